@@ -24,7 +24,7 @@ from . import build as _build_mod
 
 __all__ = ["Compressor", "CSAError", "load_library", "fp4_e4m3_roundtrip", "fp4_e8m0_roundtrip", "rope_table",
            "default_options",
-           "library_path", "ABI_FUNCTIONS"]
+           "library_path", "ABI_FUNCTIONS", "Attention", "PagedCache", "rmsnorm_residual_q8"]
 
 _lock = threading.Lock()
 _lib = None
@@ -37,7 +37,10 @@ ABI_FUNCTIONS = ("csa_options_default", "csa_compressor_create", "csa_compressor
                  "csa_fp4_e4m3_roundtrip", "csa_rope_table", "csa_set_profile_events", "csa_kernel_launches",
                  "csa_uses_tensor_cores", "csa_compress_prefill_noalloc", "csa_compress_prefill_into",
                  "csa_prefill_geometry",
-                 "csa_fp4_e8m0_roundtrip", "csa_compressor_set_gate_bias")
+                 "csa_fp4_e8m0_roundtrip", "csa_compressor_set_gate_bias",
+                 "csa_cache_append", "csa_attention_create", "csa_attention_prefill", "csa_attention_decode",
+                 "csa_attention_status", "csa_attention_launches", "csa_attention_destroy",
+                 "csa_rmsnorm_residual_q8")
 
 
 class CSAError(RuntimeError):
@@ -104,6 +107,14 @@ def load_library(build_if_missing: bool = True):
                                       ctypes.POINTER(ctypes.c_int)], I),
             "csa_compress_prefill_noalloc": ([P, P, I, I, I, I, P, P], I),
             "csa_compress_prefill_into": ([P, P, I, I, I, I, P, I, P], I),
+            "csa_cache_append": ([P, P, I, I, P, I, P, P, P, P], I),
+            "csa_attention_create": ([I, I, I, I, ctypes.c_float, P], I),
+            "csa_attention_prefill": ([P, P, P, I, I, I, I, P, P, P, P], I),
+            "csa_attention_decode": ([P, P, P, P, I, P, I, P, P, P], I),
+            "csa_attention_status": ([P, P], I),
+            "csa_attention_launches": ([P], I64),
+            "csa_attention_destroy": ([P], None),
+            "csa_rmsnorm_residual_q8": ([P, P, P, I64, I, ctypes.c_float, I, P, P, P, P, P], I),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -451,3 +462,6 @@ def state_window_start(pos: int, ratio: int, overlap: int) -> int:
         return ratio * g
     k0 = (g - 1) - ((g - 1) % 2)
     return 4 * k0
+
+
+from .layer import Attention, PagedCache, rmsnorm_residual_q8  # noqa: E402  (needs the names above)

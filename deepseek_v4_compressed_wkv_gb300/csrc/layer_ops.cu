@@ -1,0 +1,274 @@
+// The paged cache's write and the residual RMSNorm with an 8-bit output.
+#include "layer_ops.h"
+
+namespace csa {
+namespace {
+
+// ---------------------------------------------------------------------------------------
+// Cache write: entry e = b * G + i of the call's rows to index first[b] + i of sequence b.
+//
+// Bytes are moved once; one warp per entry, each array's row as units of the widest type its
+// addresses allow (a 512-wide latent is two 16-byte units a lane).  Bound by HBM (read + write)
+// for a prefill's entries, by the launch for a decode step's.
+
+struct AppendParams {
+  csa_cache cache;
+  csa_out in;
+  const int32_t* page_table;
+  const int32_t* first;
+  const uint8_t* mask;
+  int* status;
+  int B, G, max_pages;
+  int lat_unit, code_unit, scale_unit;  // bytes moved at a time: 16, 8, 4, 2 or 1
+  int lat_bytes, code_bytes, scale_bytes;
+};
+
+template <class T>
+__device__ __forceinline__ void copy_units(uint8_t* dst, const uint8_t* src, int bytes, int lane) {
+  for (int i = lane; i < bytes / (int)sizeof(T); i += 32)
+    reinterpret_cast<T*>(dst)[i] = __ldg(reinterpret_cast<const T*>(src) + i);
+}
+
+__device__ __forceinline__ void copy_row(uint8_t* dst, const uint8_t* src, int bytes, int unit, int lane) {
+  if (unit == 16)
+    copy_units<uint4>(dst, src, bytes, lane);
+  else if (unit == 8)
+    copy_units<uint2>(dst, src, bytes, lane);
+  else if (unit == 4)
+    copy_units<uint32_t>(dst, src, bytes, lane);
+  else if (unit == 2)
+    copy_units<uint16_t>(dst, src, bytes, lane);
+  else
+    copy_units<uint8_t>(dst, src, bytes, lane);
+}
+
+constexpr int kAppendWarps = 8;
+
+__global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const AppendParams P) {
+  const int lane = threadIdx.x & 31;
+  const long long e = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  if (e >= (long long)P.B * P.G) return;
+  const int b = (int)(e / P.G), i = (int)(e % P.G);
+  if (P.mask && !P.mask[b]) return;
+  const long long j = (long long)P.first[b] + i, page = j / P.cache.page_size;
+  int bad = j < 0 ? 1 : page >= P.max_pages ? 2 : 0;
+  int p = 0;
+  if (!bad) {
+    p = P.page_table[(long long)b * P.max_pages + page];
+    if (p < 0 || p >= P.cache.pages) bad = 4;
+  }
+  if (bad) {
+    if (P.status && lane == 0) atomicOr(P.status, bad);
+    return;
+  }
+  const long long row = (long long)p * P.cache.page_size + j % P.cache.page_size;
+  if (P.cache.latent)
+    copy_row((uint8_t*)P.cache.latent + row * P.lat_bytes, (const uint8_t*)P.in.latent + e * P.lat_bytes, P.lat_bytes,
+             P.lat_unit, lane);
+  if (P.cache.codes) {
+    copy_row(P.cache.codes + row * P.code_bytes, P.in.codes + e * P.code_bytes, P.code_bytes, P.code_unit, lane);
+    copy_row(P.cache.scales + row * P.scale_bytes, P.in.scales + e * P.scale_bytes, P.scale_bytes, P.scale_unit, lane);
+  }
+}
+
+int common_unit(const void* a, const void* b, int bytes) {
+  const uintptr_t u = (uintptr_t)a | (uintptr_t)b | (uintptr_t)bytes | 16;
+  return (int)(u & (~u + 1));
+}
+
+// ---------------------------------------------------------------------------------------
+// Residual addition, RMSNorm and e4m3 quantisation.
+//
+// One pass: a row is held in registers (8 features a thread and piece, piece i at feature
+// 8 * (i * T + t), so that a block's scale is a maximum over 4 or 16 adjacent threads), its sum of
+// squares and, with one scale per row, its maximum are reduced over the T threads, and every
+// output is written from the registers.  9 bytes a feature move through HBM, which bounds it; the
+// sum, the mean and the quotients are f32.
+
+struct NormParams {
+  const uint16_t* x;
+  const uint16_t* residual;
+  const float* gain;
+  uint16_t* residual_out;
+  uint16_t* y;
+  uint8_t* q;
+  void* scales;
+  long long rows;
+  int dim;
+  float eps;
+};
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t bf_pack(float lo, float hi) {
+  return (uint32_t)bf16_bits(lo) | ((uint32_t)bf16_bits(hi) << 16);
+}
+// The maximum, NaN if either is (a row's NaN shows in its scale).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxFloor = 448.0f * 1.17549435082228750797e-38f;  // 448 * 2^-126: the scale stays normal
+
+// The power-of-two scale for amax: the smallest power of two >= max(amax, floor) / 448; *byte is its
+// e8m0 encoding (255: NaN).
+__device__ __forceinline__ float e4m3_pow2_scale(float amax, uint32_t* byte) {
+  const float a = __fdiv_rn(max_nan(amax, kAmaxFloor), kE4m3Max);
+  const uint32_t u = __float_as_uint(a);
+  const uint32_t e = min((u >> 23) + ((u & 0x7FFFFFu) != 0u ? 1u : 0u), 255u);
+  *byte = e;
+  return e == 255u ? __int_as_float(0x7fffffff) : __uint_as_float(e << 23);
+}
+
+// BLOCK: features per scale (32, 128, 0 for the row).  PIECES: 8-feature pieces a thread.
+template <int BLOCK, int PIECES>
+__global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(const NormParams P) {
+  __shared__ float red[2][32];
+  const int T = blockDim.x, t = threadIdx.x, lane = t & 31, warp = threadIdx.y * (T >> 5) + (t >> 5);
+  const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  const bool live = row < P.rows;
+  const long long base = row * P.dim;
+  float s[PIECES][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int f = 8 * (i * T + t);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[i][k] = 0.0f;
+    if (!live || f >= P.dim) continue;
+    const uint4 a = *reinterpret_cast<const uint4*>(P.x + base + f);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[i][2 * k] = bf_lo(w[k]), s[i][2 * k + 1] = bf_hi(w[k]);
+    if (P.residual) {
+      const uint4 r = *reinterpret_cast<const uint4*>(P.residual + base + f);
+      const uint32_t v[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[i][2 * k] += bf_lo(v[k]), s[i][2 * k + 1] += bf_hi(v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss = fmaf(s[i][k], s[i][k], ss);
+    if (P.residual_out)
+      *reinterpret_cast<uint4*>(P.residual_out + base + f) = make_uint4(
+          bf_pack(s[i][0], s[i][1]), bf_pack(s[i][2], s[i][3]), bf_pack(s[i][4], s[i][5]), bf_pack(s[i][6], s[i][7]));
+  }
+  ss = warp_sum(ss);
+  if (T > 32) {
+    if (lane == 0) red[0][warp] = ss;
+    __syncthreads();
+    ss = 0.0f;
+    for (int w = 0; w < (T >> 5); ++w) ss += red[0][threadIdx.y * (T >> 5) + w];
+  }
+  const float inv = 1.0f / sqrtf(ss / (float)P.dim + P.eps);
+  float row_max = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int f = 8 * (i * T + t);
+    if (!live || f >= P.dim) continue;
+    const float4 g0 = *reinterpret_cast<const float4*>(P.gain + f), g1 = *reinterpret_cast<const float4*>(P.gain + f + 4);
+    const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      s[i][k] = s[i][k] * inv * g[k];
+      if (BLOCK == 0) row_max = max_nan(row_max, fabsf(s[i][k]));
+    }
+    if (P.y)
+      *reinterpret_cast<uint4*>(P.y + base + f) = make_uint4(bf_pack(s[i][0], s[i][1]), bf_pack(s[i][2], s[i][3]),
+                                                             bf_pack(s[i][4], s[i][5]), bf_pack(s[i][6], s[i][7]));
+  }
+  if (BLOCK == 0) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) row_max = max_nan(row_max, __shfl_xor_sync(0xffffffffu, row_max, o));
+    if (T > 32) {
+      if (lane == 0) red[1][warp] = row_max;
+      __syncthreads();
+      for (int w = 0; w < (T >> 5); ++w) row_max = max_nan(row_max, red[1][threadIdx.y * (T >> 5) + w]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int f = 8 * (i * T + t);
+    const bool act = live && f < P.dim;
+    float a;
+    if (BLOCK == 0) {
+      a = __fdiv_rn(max_nan(row_max, kAmaxFloor), kE4m3Max);
+      if (act && f == 0) reinterpret_cast<float*>(P.scales)[row] = a;
+    } else {
+      constexpr int kLanes = BLOCK / 8;  // adjacent threads of a block, in one warp and live together
+      float m = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = max_nan(m, fabsf(s[i][k]));
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (BLOCK == 32) {
+        uint32_t byte;
+        a = e4m3_pow2_scale(m, &byte);
+        if (act && (t & (kLanes - 1)) == 0)
+          reinterpret_cast<uint8_t*>(P.scales)[row * (P.dim / 32) + f / 32] = (uint8_t)byte;
+      } else {
+        a = __fdiv_rn(max_nan(m, kAmaxFloor), kE4m3Max);
+        if (act && (t & (kLanes - 1)) == 0) reinterpret_cast<float*>(P.scales)[row * (P.dim / 128) + f / 128] = a;
+      }
+    }
+    if (!act) continue;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = make_float2(__fdiv_rn(s[i][2 * k], a), __fdiv_rn(s[i][2 * k + 1], a));
+      w[k] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+    }
+    *reinterpret_cast<uint2*>(P.q + base + f) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  }
+}
+
+template <int BLOCK>
+cudaError_t launch_norm(const NormParams& P, cudaStream_t s) {
+  // threads of a row: a warp up to 256 features, else two pieces a thread (1024 threads at 16384)
+  const int units = P.dim / 8;
+  const int pieces = units > 32 ? 2 : 1;
+  const int T = (units + 32 * pieces - 1) / (32 * pieces) * 32;
+  const int R = T >= 256 ? 1 : min(8, 256 / T);  // rows of a CTA
+  const dim3 block(T, R), grid((unsigned)((P.rows + R - 1) / R));
+  if (pieces == 1)
+    rmsnorm_q8_kernel<BLOCK, 1><<<grid, block, 0, s>>>(P);
+  else
+    rmsnorm_q8_kernel<BLOCK, 2><<<grid, block, 0, s>>>(P);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const csa_cache& cache, const csa_out& in, int B, int G, const int32_t* page_table,
+                                int max_pages, const int32_t* first, const uint8_t* mask, int* status, cudaStream_t s) {
+  AppendParams P{};
+  P.cache = cache;
+  P.in = in;
+  P.page_table = page_table;
+  P.first = first;
+  P.mask = mask;
+  P.status = status;
+  P.B = B;
+  P.G = G;
+  P.max_pages = max_pages;
+  P.lat_bytes = cache.head_dim * 2;
+  P.code_bytes = cache.head_dim / 2;
+  P.scale_bytes = cache.head_dim / fp4_scale_block(cache.fp4);
+  P.lat_unit = common_unit(cache.latent, in.latent, P.lat_bytes);
+  P.code_unit = common_unit(cache.codes, in.codes, P.code_bytes);
+  P.scale_unit = common_unit(cache.scales, in.scales, P.scale_bytes);
+  const long long n = (long long)B * G;
+  cache_append_kernel<<<(unsigned)((n + kAppendWarps - 1) / kAppendWarps), kAppendWarps * 32, 0, s>>>(P);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rmsnorm_residual_q8(const uint16_t* x, const uint16_t* residual, const float* gain, long long rows,
+                                       int dim, float eps, int scale_block, uint16_t* residual_out, uint16_t* y,
+                                       uint8_t* q, void* scales, cudaStream_t s) {
+  NormParams P{x, residual, gain, residual_out, y, q, scales, rows, dim, eps};
+  return scale_block == 32 ? launch_norm<32>(P, s) : scale_block == 128 ? launch_norm<128>(P, s) : launch_norm<0>(P, s);
+}
+
+}  // namespace csa

@@ -1,0 +1,42 @@
+// Launchers of the operators around the compressor (host side, enqueue only).
+#pragma once
+
+#include "csa_internal.cuh"
+
+namespace csa {
+
+// Arguments of one attention call.  Prefill: token i of sequence b is row b * N + i of q and out,
+// at position start + i, over rows 0 .. start + i of kv [B][kv_rows][D].  Decode (page_table in
+// use, N = 1): the token is at position lens[b] - 1 over the cache's entries.
+struct AttnCall {
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;           // may be null
+  const int32_t* lens;  // decode: entries; prefill: tokens, may be null
+  const uint16_t* kv;   // prefill's rows
+  csa_cache cache;      // decode's entries
+  const int32_t* page_table;
+  int max_pages;
+  bool paged;
+  int B, N, start, kv_rows;
+};
+
+cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_t s);
+size_t attention_workspace_bytes(int head_dim);
+
+cudaError_t launch_cache_append(const csa_cache& cache, const csa_out& in, int B, int G, const int32_t* page_table,
+                                int max_pages, const int32_t* first, const uint8_t* mask, int* status, cudaStream_t s);
+
+cudaError_t launch_rmsnorm_residual_q8(const uint16_t* x, const uint16_t* residual, const float* gain, long long rows,
+                                       int dim, float eps, int scale_block, uint16_t* residual_out, uint16_t* y,
+                                       uint8_t* q, void* scales, cudaStream_t s);
+
+}  // namespace csa
+
+struct csa_attention {
+  int heads, D, window, sinks, device;
+  float scale;
+  int* dev_flag;       // device-side error flag
+  uint8_t* workspace;  // partial results of split sequences
+  long long launches;  // kernels enqueued so far
+};

@@ -315,6 +315,123 @@ int csa_prefill_geometry(const csa_compressor* c, int B, int N, int start_pos, i
  * double precision and rounded once to f32. */
 int csa_rope_table(const csa_options* opt, int pos0, int npos, float* cos_out, float* sin_out);
 
+/* ---- The attention layer around the compressor ------------------------------------------
+ *
+ * The operators that a serving layer runs next to the compressor: the residual RMSNorm that makes
+ * its x, the paged cache its entries go to, and attention over one shared key/value row per
+ * position, the form of the compressed layers (every query head reads the same latent, as key and
+ * as value), for a prompt's exact recent window and for one new token over a paged cache.
+ *
+ *   visible(t)  = { j <= t : j < sinks or j > t - window }, every j <= t when window is 0
+ *   S[h][j]     = scale * <q[t][h], c[j]>             c[j]: row j of the cache
+ *   lse[t][h]   = ln sum_j exp S[h][j]                over the visible j
+ *   out[t][h]   = sum_j exp(S[h][j] - lse[t][h]) c[j]
+ *   no visible j: out = 0, lse = -inf
+ *
+ * Scores, softmax statistics and sums are f32; the weights exp(S - running maximum) are rounded to
+ * bf16 for the second product and out is rounded to bf16 once.  Rows that are not visible to a
+ * query are not read for it: what they hold (NaN, infinities) cannot reach its result. */
+
+/* A paged cache of entries (dev arrays owned by the caller): page p, slot s is row
+ * p * page_size + s of each array, in csa_out's element layouts.  latent holds the entries' bf16
+ * values; codes and scales hold e2m1 codes with e4m3 scales per 16 features (fp4 = 1) or
+ * power-of-two scales per 32 (fp4 = 2).  Either may be absent (NULL).  Entry j of a sequence is
+ * slot j % page_size of page page_table[sequence][j / page_size].  A compressed-KV cache written by
+ * csa_compress_prefill_into is one too: page_size = cache_rows and page b for sequence b. */
+typedef struct {
+  uint16_t* latent;
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t pages;  /* pages in each array */
+  int page_size;  /* entries per page, >= 1 (any number) */
+  int head_dim;   /* features per entry */
+  int fp4;        /* format of codes and scales: 1 or 2 (as the compressor's option) */
+} csa_cache;
+
+/* Writes entries (csa_out rows as a compressor call leaves them, row b * G + i) to the cache: entry
+ * i of sequence b goes to index first[b] + i, for the sequences with mask[b] != 0.
+ *  in          the arrays that the cache has are read (dev); prequant is not used
+ *  page_table  [B][max_pages] int32 dev
+ *  first       [B] int32 dev: index of the sequence's first new entry
+ *  mask        [B] u8 dev or NULL (all): e.g. the emitted flags of a decode step
+ *  status      one int dev or NULL: bits are set (never cleared) where an entry was left out: 1 a
+ *              negative index, 2 an index beyond the page table, 4 a page outside the cache
+ * head_dim must be a multiple of 16 in [16, 512].  Two entries of one call for the same slot race.
+ * Returns CSA_OK or a negative csa_status. */
+int csa_cache_append(const csa_cache* cache, const csa_out* in, int B, int G, const int32_t* page_table, int max_pages,
+                     const int32_t* first, const uint8_t* mask, int* status, csa_stream_t stream);
+
+typedef struct csa_attention csa_attention;
+
+/* Creates an attention instance: heads query heads over rows of head_dim features, with a window of
+ * the last `window` positions (0: all) and the first `sinks` positions always visible (no effect
+ * without a window).  scale multiplies the scores; 0 selects 1 / sqrt(head_dim).
+ * Requirements: 1 <= heads <= 1024, head_dim a multiple of 64 in [64, 512], window >= 0,
+ * sinks >= 0, scale finite and >= 0.
+ * Allocates the workspace for split sequences on the current device, which becomes the handle's
+ * device.  Calls allocate nothing afterwards and can be captured into CUDA graphs after a first
+ * call on the device.  A handle's calls share its workspace: order them on the device (one stream,
+ * or events; graphs captured from one handle are replayed one after the other). */
+int csa_attention_create(int heads, int head_dim, int window, int sinks, float scale, csa_attention** out);
+
+/* Attention for the tokens start_pos .. start_pos + N - 1 of B sequences (a prompt, or a chunk of
+ * one), each over its own rows.
+ *  q    [B][N][heads][head_dim] bf16 dev
+ *  kv   [B][kv_rows][head_dim] bf16 dev: row j is position j; kv_rows >= start_pos + N
+ *  lens [B] int32 dev or NULL: tokens of sequence b in this call (a padded batch); outputs of the
+ *       tokens at and past lens[b] are left as they were (a length outside [0, N] is taken as the
+ *       nearest end and raises flag bit 1, see csa_attention_status)
+ *  out  [B][N][heads][head_dim] bf16 dev
+ *  lse  [B][N][heads] f32 dev or NULL
+ * q, kv and out must be 16-byte aligned.  Returns CSA_OK or a negative csa_status. */
+int csa_attention_prefill(csa_attention* a, const uint16_t* q, const uint16_t* kv, int B, int N, int start_pos,
+                          int kv_rows, const int32_t* lens, uint16_t* out, float* lse, csa_stream_t stream);
+
+/* Attention of one new token of each of B sequences over a paged cache (reads latent if the cache
+ * has it, else codes and scales, which must be fp4 = 1).
+ *  q          [B][heads][head_dim] bf16 dev
+ *  page_table [B][max_pages] int32 dev (may be NULL when max_pages is 0)
+ *  lens       [B] int32 dev: entries of sequence b; its query is at position lens[b] - 1
+ *  out        [B][heads][head_dim] bf16 dev
+ *  lse        [B][heads] f32 dev or NULL
+ * A sequence's entries are split over the GPU and joined.  A length that is negative or beyond the
+ * page table is taken as the nearest end and raises flag bit 1; an entry on a page outside the
+ * cache is not read, raises flag bit 2 and leaves that sequence's results undefined.
+ * q, out and the cache's arrays must be 16-byte aligned.  Returns CSA_OK or a negative csa_status. */
+int csa_attention_decode(csa_attention* a, const uint16_t* q, const csa_cache* cache, const int32_t* page_table,
+                         int max_pages, const int32_t* lens, int B, uint16_t* out, float* lse, csa_stream_t stream);
+
+/* Reads and clears the handle's device flag (synchronises the stream): CSA_OK, CSA_ERR_TIMEOUT
+ * (bit 4: a device-side wait ran out; that call's outputs are undefined, the handle stays usable)
+ * or CSA_ERR_DEVICE (bit 1 a length out of range, bit 2 a page outside the cache, bit 8, only in
+ * the bounds-checked build, a store outside its buffer, skipped). */
+int csa_attention_status(csa_attention* a, csa_stream_t stream);
+
+/* Number of kernels the handle has enqueued since it was created. */
+int64_t csa_attention_launches(const csa_attention* a);
+
+/* Frees the handle and its device memory (synchronises the device first). NULL is a no-op. */
+void csa_attention_destroy(csa_attention* a);
+
+/* Residual addition, RMSNorm and quantisation to 8 bits of rows of a token stream, in one pass:
+ *   s = x + residual (f32);  n = s * (mean(s^2) + eps)^-1/2 * gain
+ *   residual_out = bf16(s), y = bf16(n), q = e4m3(n / a), scales = a of each block
+ *  x, residual   [rows][dim] bf16 dev; residual may be NULL (s = x)
+ *  gain          [dim] f32 dev
+ *  scale_block   features per scale: 128 or 0 (one per row): a = max(amax, 448 * 2^-126) / 448 in f32;
+ *                32: the smallest power of two >= that, as its e8m0 byte (2^(byte - 127))
+ *  residual_out  [rows][dim] bf16 dev or NULL; may be residual (or x) itself
+ *  y             [rows][dim] bf16 dev or NULL: e.g. the compressor's x
+ *  q             [rows][dim] e4m3 dev: round to nearest even, saturating at 448
+ *  scales        [rows][dim / scale_block] f32, or u8 with scale_block 32, dev
+ * The quotient is an IEEE f32 division.  A row with a NaN or an infinity gives what the formula
+ * gives (NaN; a NaN block has a NaN scale, e8m0 byte 255).
+ * Requirements: dim a multiple of scale_block and of 32, at most 16384; arrays 16-byte aligned
+ * (scales 4).  rows may be 0 (nothing is enqueued). */
+int csa_rmsnorm_residual_q8(const uint16_t* x, const uint16_t* residual, const float* gain, int64_t rows, int dim,
+                            float eps, int scale_block, uint16_t* residual_out, uint16_t* y, uint8_t* q, void* scales,
+                            csa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
