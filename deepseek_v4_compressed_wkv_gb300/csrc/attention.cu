@@ -1,20 +1,28 @@
 // Attention over one shared key/value row per position (see include/csa.h): a prompt's tokens over
 // their own rows with a window and sinks, or one new token a sequence over a paged cache.
 //
-// An item is one token's up to 64 query heads.  Its visible rows c_0, c_1, .. (the sinks, then the
-// window; hidden rows are never loaded) are taken 64 at a time:
+// A sequence's queries are its N tokens' heads in order, [N * H][D]; an item is 64 of them (one
+// token's at H = 64, four tokens' at H = 16, half a token's at H = 128), over the rows that any of
+// its tokens sees: the sinks, then the window.  Those rows are taken 64 at a time:
 //
-//   S^T = C Q^T   [64 rows x 64 heads], features as the K dimension
-//   P   = exp2(S^T * scale - m)         m: the running maximum of each head
-//   O^T = O^T + C^T P                   [D features x 64 heads], rows as the K dimension
+//   S^T = C Q^T   [64 rows x 64 queries], features as the K dimension
+//   P   = exp2(S^T * scale - m)           m: the running maximum of each query
+//   O^T = O^T + C^T P                     [D features x 64 queries], rows as the K dimension
 //
-// Transposed, both products keep the rows' tile as the A operand, once K-major (64 x D) and once
-// M-major (D x 64): one copy in shared memory serves as key and as value, which is what a shared
-// row offers, and O^T takes D / 128 * 64 columns of tensor memory (256 of 512 at D = 512) where O
-// with heads as rows would take all of it for half a filled tile.  The scores come back with a
-// row (key) per TMEM lane in the matrix-fragment shape, where the maximum over rows is three
-// shuffles.  That maximum is only renewed (and O^T, l scaled) when a score passes it by 2^8:
-// the weights then stay below 2^8 in bf16, whose relative precision does not depend on it.
+// Transposed, both products take the rows' tile as their A operand, once K-major (64 x D) and once
+// M-major (D x 64): one copy in shared memory is key and value, which is what a shared row offers,
+// and O^T takes D / 128 * 64 columns of tensor memory (256 of 512 at D = 512) where queries as rows
+// would take all of it.  The scores come back with a row per TMEM lane in the matrix-fragment shape,
+// where the maximum over rows is three shuffles.  That maximum is only renewed (and O^T, l scaled)
+// when a score passes it by 2^8: the weights then stay below 2^8 in bf16, whose relative precision
+// does not depend on it.
+//
+// What bounds it (probes on GB300, cycles): a 64 x 64 x 16 MMA takes 32 and a 128 x 64 x 16 one 48
+// (shared-memory reads of both operands at 128 bytes a cycle), so a tile of 64 rows at D = 512 costs
+// 1024 + 768; its 64 KB arrive from HBM in 2510 (26 bytes a cycle and SM, 7.2 TB/s).  Decode over
+// latents is therefore bound by HBM, over codes (18 KB a tile) by the MMAs' operand reads.  Rows
+// come by 16-byte cp.async, which takes any page size and leaves hidden rows out (zeros) at the rate
+// of tiled TMA boxes (760 cycles a tile from L2, against 8010 for four-row TMA gathers).
 //
 // Work is cut by tiles: the call's tiles, in item order, are divided evenly over the CTAs, so ragged
 // lengths and few long sequences fill the GPU alike; an item cut by a CTA boundary leaves partial
@@ -22,6 +30,7 @@
 // kJoinTiles tiles the boundaries are moved to item starts instead: the imbalance costs less than
 // pieces and their join.
 #include <atomic>
+#include <cstdlib>
 
 #include "layer_ops.h"
 #include "tc_common.cuh"
@@ -32,87 +41,90 @@ namespace {
 using namespace tcx;
 
 constexpr int kTile = 64;                      // rows of a tile
-constexpr int kHeads = 64;                     // heads of an item
+constexpr int kCols = 64;                      // queries of an item
 constexpr int kChunkBytes = 8192;              // 64 rows x 64 features bf16: one column of swizzled atoms
-constexpr int kPBytes = kTile * kHeads * 2;    // one weights buffer
-constexpr int kSoftWarps = 4, kSoftThreads = 128;
-constexpr int kMmaWarp = 4, kQWarp = 5, kProdWarp = 6;
+constexpr int kPBytes = kTile * kCols * 2;     // one weights buffer
+constexpr int kStageOut = 2048;                // a warp's staging of 32 queries x 32 features bf16
 constexpr int kJoinTiles = 6;   // items longer than this are split
 constexpr int kMinTiles = 4;    // a split call gives a CTA at least this many tiles
 constexpr float kStep = 8.0f;   // base-2 steps a score may pass the running maximum by
 constexpr float kFloor = -1e38f;  // running maximum while no score was seen
 constexpr int kSpins = 1 << 16;   // polls of two barriers before the MMA warp waits for one of them
-constexpr int kAuxBytes = 3072;   // barriers, flags, per-warp maxima and sums
+constexpr int kAuxBytes = 3584;   // barriers, flags, per-warp maxima and sums
 
 struct AttnParams {
   AttnCall c;
-  int H, D, window, sinks, hblocks;
-  long long toks;   // tokens: B * N
+  int H, D, window, sinks;
+  int per, items;    // items of a sequence, of the call
   float scale_log2;  // scale * log2(e): scores in base-2 exponents
   int* flag;
-  float* part;       // pieces: [2 * grid][64][D] f32
-  float2* part_ml;   // (maximum, sum) of each piece and head [2 * grid][64]
+  float4* part;      // pieces: [2 * grid][64 * D / 4] f32, in the order of the fragment loads
+  float2* part_ml;   // (maximum, sum) of each piece and query [2 * grid][64]
   int2* record;      // per CTA: (item, pieces) of an item whose first piece it made, or (-1, 0)
   int stages;
   uint32_t unit_magic;  // ceil(2^32 / (D / 32)): units of a row of codes
   bool split;        // items may be cut (the join kernel follows)
+#ifdef CSA_DEBUG_BOUNDS
+  uint64_t wait_ns;  // the time-out test shortens the waits
+  int test_stall;    // and leaves out each CTA's last tile
+#endif
 };
 
-// ---- the rows a token sees
+// ---- the rows an item sees
 struct Seen {
-  int b;          // sequence
-  long long cnt;  // visible rows; row v of them is position v, or v + jump from the sinks on
-  long long jump;
-  bool skip;      // padding: no output
+  int b;                // sequence
+  int f0, cols;         // first query, queries with an output (0: padding)
+  int tlo, thi;         // positions of its first and last token (thi -1: a sequence without entries)
+  int cnt;              // rows: row v is position v, or v + jump from the sinks on
+  int jump;
 };
 
-__device__ __forceinline__ Seen seen_rows(const AttnParams& P, long long tok) {
+__device__ __forceinline__ Seen seen_rows(const AttnParams& P, int item) {
   Seen s;
-  long long t;
-  s.skip = false;
+  s.b = item / P.per;
+  s.f0 = (item - s.b * P.per) * kCols;
   if (P.c.paged) {
-    s.b = (int)tok;
-    const long long top = (long long)P.c.max_pages * P.c.cache.page_size, n = __ldg(P.c.lens + tok);
-    t = (n < 0 ? 0 : n > top ? top : n) - 1;
+    const int top = P.c.max_pages * P.c.cache.page_size, n = __ldg(P.c.lens + s.b);
+    s.cols = min(kCols, P.H - s.f0);
+    s.tlo = s.thi = min(max(n, 0), top) - 1;
   } else {
-    const uint32_t b = (uint32_t)tok / (uint32_t)P.c.N, i = (uint32_t)tok - b * (uint32_t)P.c.N;
-    s.b = (int)b;
-    s.skip = P.c.lens && (int)i >= __ldg(P.c.lens + b);
-    t = (long long)P.c.start + i;
+    const int n = P.c.lens ? min(max(__ldg(P.c.lens + s.b), 0), P.c.N) : P.c.N;
+    s.cols = max(0, min(kCols, n * P.H - s.f0));
+    s.tlo = P.c.start + s.f0 / P.H;
+    s.thi = P.c.start + (s.f0 + max(s.cols, 1) - 1) / P.H;
   }
-  const long long most = (long long)P.window + P.sinks;
-  const bool all = P.window == 0 || t + 1 <= most;
-  s.cnt = all ? t + 1 : most;
-  s.jump = all ? 0 : t + 1 - most;
+  // every token from tlo on sees the rows after thi - most and the sinks at most
+  const long long most = (long long)P.window + (s.thi - s.tlo) + P.sinks;
+  const bool all = P.window == 0 || s.thi + 1 <= most;
+  s.cnt = all ? s.thi + 1 : (int)most;
+  s.jump = all ? 0 : s.thi + 1 - (int)most;
   return s;
 }
-__device__ __forceinline__ long long tiles_of(const Seen& s) {
-  return s.skip ? 0 : s.cnt <= kTile ? 1 : (s.cnt + kTile - 1) / kTile;  // an empty item still has its output
+__device__ __forceinline__ int tiles_of(const Seen& s) {
+  return s.cols == 0 ? 0 : max(1, (s.cnt + kTile - 1) / kTile);  // a sequence without entries still has its output
 }
 
 // A CTA's work: `left` tiles from tile `tile` of item `item` on.  next() gives the next segment: a
 // run of tiles of one item.
 struct Segment {
-  long long tok, t0, t1, tiles;
-  int hb;
+  int item, t0, t1, tiles;
   Seen s;
 };
 struct Walk {
-  long long tok, tile, left;
-  int hb;
+  int item, tile;
+  long long left;
   __device__ __forceinline__ bool next(const AttnParams& P, Segment& g) {
     if (left <= 0) return false;
-    for (;; ++tok, tile = 0, hb = 0) {  // over padding
-      if (tok >= P.toks) return false;  // only if the lengths changed under the kernel
-      g.s = seen_rows(P, tok);
+    for (;; ++item, tile = 0) {  // over padding
+      if (item >= P.items) return false;  // only if the lengths changed under the kernel
+      g.s = seen_rows(P, item);
       g.tiles = tiles_of(g.s);
       if (tile < g.tiles) break;
     }
-    g.tok = tok, g.hb = hb, g.t0 = tile;
-    g.t1 = min(g.tiles, tile + left);
+    g.item = item++, g.t0 = tile;
+    g.t1 = (int)min((long long)g.tiles, tile + left);
     left -= g.t1 - tile;
     tile = 0;
-    if (++hb == P.hblocks) hb = 0, ++tok;
     return true;
   }
 };
@@ -155,6 +167,16 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)
       : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+// The same over 32 columns, not waiting.
+__device__ __forceinline__ void tmem_ld_half(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 template <bool kTrans>
 __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   if constexpr (kTrans)
@@ -186,15 +208,23 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// The softmax warps' barrier; or_ gives every thread whether any passed true.
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
-__device__ __forceinline__ bool soft_or(bool p) {
+// A barrier of four warps (1: softmax, 2: epilogue); group_or gives every thread whether any passed
+// true.
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool group_or(int id, bool p) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)p), "n"(kSoftThreads)
+      : "r"((uint32_t)p), "r"(id)
       : "memory");
+  return r != 0;
+}
+// One lane of a converged warp, the same at every call: what it alone issues stays in uniform
+// registers (an MMA issued under `lane == 0` cost 70 to 126 cycles in descriptor moves, 32 this way).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -225,29 +255,34 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t scale2) {
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// ---- the kernel: warps 0-3 softmax and epilogue (TMEM lane quarter = warp), 4 MMA issue, 5 the
-// queries' copies, 6.. the rows' copies, in two groups that take alternate tiles (so that one
-// group's tile can be in flight while the other waits for its stage)
-template <bool kFp4>
-constexpr int prod_warps() {
-  return kFp4 ? 8 : 4;
-}
-template <bool kFp4>
-constexpr int attn_threads() {
-  return (kProdWarp + prod_warps<kFp4>()) * 32;
-}
+// ---- the kernel's warps: 0-3 softmax (TMEM lane quarter = warp); with one CTA an SM 4-7 the
+// epilogue, which reads O^T while the softmax warps go on with the next item (up to D = 192 two CTAs
+// share an SM instead, whose softmax warps read their own O^T); then one that issues the MMAs, one
+// for the queries' copies, and the rows' warps in two groups that take alternate tiles (one group's
+// tile can be in flight while the other waits for its stage).
+template <bool kFp4, int kCtas>
+struct Roles {
+  static constexpr bool kEpi = kCtas == 1;
+  static constexpr int kMma = kEpi ? 8 : 4, kQ = kMma + 1, kRows = kMma + 2;
+  static constexpr int kRowWarps = kFp4 ? 8 : kCtas == 2 ? 2 : 4;
+  static constexpr int kGroupWarps = kRowWarps / 2;
+  static constexpr int kTileRows = kTile / kGroupWarps;  // rows of a tile a warp brings
+  static constexpr int kThreads = 32 * (kRows + kRowWarps);
+};
 
 template <bool kFp4, int kCtas>
-__global__ void __launch_bounds__(attn_threads<kFp4>(), kCtas)
+__global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     attention_kernel(const __grid_constant__ CUtensorMap map_q, const AttnParams P) {
+  using R = Roles<kFp4, kCtas>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const int D = P.D, chunks = D / 64, nst = P.stages;
   const int stage_bytes = chunks * kChunkBytes;
   uint8_t* sQ = smem;
   uint8_t* sC = sQ + chunks * kChunkBytes;
-  uint8_t* sP = sC + nst * stage_bytes;  // two weights buffers; the epilogue's staging
-  uint8_t* aux = sP + 2 * kPBytes;
+  uint8_t* sP = sC + nst * stage_bytes;  // two weights buffers
+  uint8_t* sO = sP + 2 * kPBytes;        // the epilogue's staging, 2 KB a warp
+  uint8_t* aux = sO + 4 * kStageOut;
   uint64_t* c_full = (uint64_t*)aux;  // [8] a stage's rows have landed
   uint64_t* c_empty = c_full + 8;     // [8] a stage's products are done
   uint64_t* s_full = c_empty + 8;     // [2] scores ready
@@ -256,57 +291,68 @@ __global__ void __launch_bounds__(attn_threads<kFp4>(), kCtas)
   uint64_t* q_full = pv_done + 2;
   uint64_t* q_empty = q_full + 1;
   uint64_t* o_empty = q_empty + 1;    // O^T has been read
-  uint64_t* mma_done = o_empty + 1;   // clean-up after an abort
+  uint64_t* l_full = o_empty + 1;     // the item's maxima and sums are in `fin`
+  uint64_t* l_empty = l_full + 1;     // and have been read
+  uint64_t* mma_done = l_empty + 1;   // clean-up after an abort
   uint32_t* tmem_slot = (uint32_t*)(mma_done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
-  int* q_loads = (int*)(tmem_slot + 2);
-  long long* work = (long long*)(aux + 320);  // first token, first tile, tiles, first head block, tile index, total
-  float* red = (float*)(aux + 512);           // [2][4][64] per-warp maxima, sums; the scan's sums before
-  static_assert(512 + 2 * 4 * 64 * 4 <= kAuxBytes, "aux region");
+  int* q_loads = (int*)(tmem_slot + 2);  // copies issued, for the clean-up
+  long long* work = (long long*)(aux + 320);  // first tile's item, tile, tiles, tile index, end, total, CTAs
+  float* red = (float*)(aux + 512);   // [4][64] per-warp maxima; the scan's sums before
+  float* fin = red + 256;             // [4][64] per-warp sums, [64] maxima
+  float* inv = fin + 320;             // [64] 1 / sum
+  int* colt = (int*)(inv + 64);       // [64] the queries' positions
+  static_assert(512 + (256 + 320 + 64 + 64) * 4 <= kAuxBytes, "aux region");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kThreads = attn_threads<kFp4>();
-  constexpr int kGroupWarps = prod_warps<kFp4>() / 2;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+#ifdef CSA_DEBUG_BOUNDS
+  const uint64_t kWait = P.wait_ns;
+#else
+  constexpr uint64_t kWait = kWaitNs;
+#endif
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 8; ++s) {
-      mbar_init(&c_full[s], kGroupWarps);
+      mbar_init(&c_full[s], R::kGroupWarps);
       mbar_init(&c_empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kSoftWarps);
+      mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    mbar_init(o_empty, kSoftWarps);
+    mbar_init(o_empty, 4);
+    mbar_init(l_full, 4);
+    mbar_init(l_empty, 4);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     *q_loads = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     prefetch_map(&map_q);
   }
-  const uint32_t oc = (uint32_t)((D + 127) / 128) * kHeads;  // columns of O^T; two score buffers follow
-  const uint32_t tmem_cols = oc + 2 * kHeads <= 256 ? 256 : 512;
-  if (warp == kMmaWarp) tmem_alloc(tmem_slot, tmem_cols);
+  const uint32_t oc = (uint32_t)((D + 127) / 128) * kCols;  // columns of O^T; two score buffers follow
+  const uint32_t tmem_cols = oc + 2 * kCols <= 256 ? 256 : 512;
+  if (warp == R::kMma) tmem_alloc(tmem_slot, tmem_cols);
   griddep_launch_dependents();
 
-  // ---- the CTA's share of the call's tiles: every CTA adds up the tokens' tiles (threads over
-  // contiguous tokens) and finds its own first one
+  // ---- the CTA's share of the call's tiles: every CTA adds up the items' tiles (threads over
+  // contiguous items) and finds its own first one
   {
-    const long long per = (P.toks + kThreads - 1) / kThreads, lo = min(P.toks, per * threadIdx.x),
-                    hi = min(P.toks, lo + per);
-    long long sum = 0, top = 0;
-    for (long long i = lo; i < hi; ++i) {
-      const long long n = tiles_of(seen_rows(P, i));
+    const int per = (P.items + R::kThreads - 1) / R::kThreads, lo = min(P.items, per * (int)threadIdx.x),
+              hi = min(P.items, lo + per);
+    long long sum = 0;
+    int top = 0;
+    for (int i = lo; i < hi; ++i) {
+      const int n = tiles_of(seen_rows(P, i));
       sum += n;
       top = max(top, n);
     }
     if (blockIdx.x == 0 && P.c.lens) {  // lengths out of range are taken as the nearest end
-      const long long most = P.c.paged ? (long long)P.c.max_pages * P.c.cache.page_size : P.c.N;
-      for (int b = threadIdx.x; b < P.c.B; b += kThreads) {
-        const long long n = P.c.lens[b];
+      const int most = P.c.paged ? P.c.max_pages * P.c.cache.page_size : P.c.N;
+      for (int b = threadIdx.x; b < P.c.B; b += R::kThreads) {
+        const int n = P.c.lens[b];
         if (n < 0 || n > most) atomicOr(P.flag, 1);
       }
     }
@@ -317,132 +363,227 @@ __global__ void __launch_bounds__(attn_threads<kFp4>(), kCtas)
       top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     }
     long long* ws = (long long*)red;  // [warp] sums, then [warp] maxima
-    if (lane == 31) ws[warp] = pre, ws[16 + warp] = top;
-    if (threadIdx.x == 0) work[0] = P.toks, work[1] = 0, work[2] = 0, work[3] = 0, work[4] = 0;
+    if (lane == 31) ws[warp] = pre, ws[32 + warp] = top;
     __syncthreads();
     long long before = 0, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < R::kThreads / 32; ++w) {
       if (w < warp) before += ws[w];
       total += ws[w];
-      top = max(top, ws[16 + w]);
+      top = max(top, (int)ws[32 + w]);
     }
-    pre += before - sum;  // tokens' tiles before this thread's
-    const int hbs = P.hblocks;
-    total *= hbs;
+    pre += before - sum;  // tiles before this thread's items
     const bool cut = P.split && top > kJoinTiles;
     const long long ctas = cut ? min((long long)gridDim.x, max(1LL, total / kMinTiles)) : gridDim.x;
     const long long i = blockIdx.x;
     const long long a = i < ctas ? total * i / ctas : total, e = i < ctas ? total * (i + 1) / ctas : total;
-    // the boundary x: the item it falls in and, without cutting, the start of the first item from it on
+    if (threadIdx.x == 0) work[0] = P.items, work[1] = 0, work[3] = work[4] = total, work[5] = total, work[6] = ctas;
+    __syncthreads();
+    // the boundary x: the item it falls in or, without cutting, the first item that starts from it on
     auto locate = [&](long long x, bool first) {
-      if (sum == 0 || x < pre * hbs || x >= (pre + sum) * hbs) return;
-      long long at = pre * hbs;
-      for (long long tok = lo; tok < hi; ++tok) {
-        const long long n = tiles_of(seen_rows(P, tok));
-        if (n == 0 || x >= at + n * hbs) {
-          at += n * hbs;
+      if (x < pre || x >= pre + sum) return;
+      long long at = pre;
+      for (int item = lo; item < hi; ++item) {
+        const int n = tiles_of(seen_rows(P, item));
+        if (x >= at + n) {
+          at += n;
           continue;
         }
-        const int hb = (int)((x - at) / n);
-        long long start = at + hb * n, tile = x - start;
-        long long t = tok, h = hb;
-        if (!cut && tile > 0) {
-          start += n, tile = 0;
-          if (++h == hbs) h = 0, ++t;
-        }
+        int tile = (int)(x - at);
+        if (!cut && tile > 0) at += n, tile = 0, ++item;
         if (first)
-          work[0] = t, work[1] = tile, work[3] = h, work[4] = start + tile;
+          work[0] = item, work[1] = tile, work[3] = at + tile;
         else
-          work[5] = start + tile;
+          work[4] = at + tile;
         return;
       }
     };
-    if (threadIdx.x == 0) work[4] = work[5] = total;
-    __syncthreads();
     locate(a, true);
     locate(e, false);
     __syncthreads();
     if (threadIdx.x == 0) {
-      work[2] = work[5] - work[4];
-      work[6] = total;
-      work[7] = ctas;
+      work[2] = work[4] - work[3];
       if (P.split) P.record[blockIdx.x] = make_int2(-1, 0);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  Walk walk{work[0], work[1], work[2], (int)work[3]};
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  Walk walk{(int)work[0], (int)work[1], work[2]};
   Segment g;
 
-  if (warp >= kProdWarp) {
-    // ---- rows: warp w of a group takes rows kRows * w .. of its group's tiles
-    constexpr int kRows = kTile / kGroupWarps;
-    const int grp = (warp - kProdWarp) / kGroupWarps, w = (warp - kProdWarp) % kGroupWarps;
-    const uint16_t* base = P.c.paged ? P.c.cache.latent : P.c.kv;
+  // ---- an item's end, by the four warps that own O^T's lane quarters (w = warp % 4): the sums over
+  // rows in `fin`, O^T (complete with tile kl) scaled to out, or left as a piece.  False after an abort.
+  auto finish = [&](int w, int bar, const Segment& g, uint32_t seg, uint32_t kl, long long index, int tid) -> bool {
+    bool ok = !R::kEpi || mbar_wait(l_full, seg & 1, abort_flag, kWait);
+    ok = ok && mbar_wait(&pv_done[kl & 1], (kl >> 1) & 1, abort_flag, kWait);
+    if (group_or(bar, !ok)) return false;
+    tc_fence_after();
+    const bool whole = g.t0 == 0 && g.t1 == g.tiles;
+    // a piece: slot 0 of the CTA for its first segment's, 1 for its last's (an item's first piece)
+    const int slot = 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0);
+    const long long orow = (long long)g.s.b * P.c.N * P.H + g.s.f0, rows = (long long)P.c.B * P.c.N * P.H;
+    if (tid < kCols) {
+      const float l = (fin[tid] + fin[64 + tid]) + (fin[128 + tid] + fin[192 + tid]), m = fin[256 + tid];
+      if (whole) {
+        float r, lg;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(l));
+        asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(l));
+        inv[tid] = l == 0.0f ? 0.0f : r;
+        if (P.c.lse && tid < g.s.cols && in_bounds(orow + tid, rows, P.flag))
+          P.c.lse[orow + tid] = l == 0.0f ? -INFINITY : (m + lg) * 0.693147180559945f;
+      } else {
+        P.part_ml[slot * kCols + tid] = make_float2(m, l);
+      }
+    }
+    group_sync(bar);
+    if (R::kEpi && lane == 0) mbar_arrive(l_empty);
+    const uint32_t base = tmem + ((uint32_t)(32 * w) << 16);
+    if (whole) {
+      const uint32_t stage = smem_addr(sO) + w * kStageOut;
+      for (int x = 0; x < chunks; x += 2) {
+        const int halves = x + 1 < chunks ? 2 : 1;  // 16 lanes (features) each: 32 w + 16 h, or 16 w of 64
+        const int d = x * 64 + w * 16 * halves;
+        for (int c = 0; c < 2; ++c) {  // 32 queries at a time
+          uint32_t o[2][16];
+          const uint32_t at = base + (x >> 1) * kCols + 32 * c;
+          tmem_ld_half(at, o[0]);
+          if (halves == 2) tmem_ld_half(at + (16u << 16), o[1]);
+          tmem_ld_wait();
+          // to [query][32 features] by transposed stores; 16-byte units swizzled against conflicts
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == halves) break;
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              uint32_t v[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int q = i + (j >> 1);
+                const float2 f = *reinterpret_cast<const float2*>(inv + 32 * c + 8 * q + 2 * (lane & 3));
+                v[j] = bf16x2(__uint_as_float(o[h][4 * q + 2 * (j & 1)]) * f.x,
+                              __uint_as_float(o[h][4 * q + 2 * (j & 1) + 1]) * f.y);
+              }
+              const int r = 8 * (i + (lane >> 4)) + (lane & 7), u = 2 * h + ((lane >> 3) & 1);
+              stmatrix4<true>(stage + r * 64 + ((u ^ ((r >> 1) & 3)) << 4), v[0], v[1], v[2], v[3]);
+            }
+          }
+          __syncwarp();
+          const int u = lane & 3;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = (lane >> 2) + 8 * i, q = 32 * c + r;
+            if (u < 2 * halves && q < g.s.cols && in_bounds(orow + q, rows, P.flag))
+              *reinterpret_cast<uint4*>(P.c.out + (orow + q) * D + d + 8 * u) =
+                  *reinterpret_cast<const uint4*>(sO + w * kStageOut + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+          }
+          __syncwarp();
+        }
+      }
+    } else {
+      float4* dst = P.part + (size_t)slot * (kCols * D / 4) + lane;
+      for (int x = 0; x < chunks; ++x) {  // half h of 16 lanes a warp of the block of 128 features
+        const int blk = x >> 1, h = x & 1;
+        uint32_t o[32];
+        tmem_ld_frag(base + blk * kCols + ((uint32_t)(16 * h) << 16), o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          dst[((x * 4 + w) * 8 + i) * 32] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                        __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+      }
+      if (g.t0 == 0 && tid == 0) {
+        // the item ends in the CTA whose share holds its last tile
+        const long long end = index + g.tiles, total = work[5], ctas = work[6];
+        long long j = (end * ctas - 1) / total;
+        while (total * (j + 1) / ctas < end) ++j;
+        while (total * j / ctas >= end) --j;
+        P.record[blockIdx.x] = make_int2(g.item, (int)(j - blockIdx.x) + 1);
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(o_empty);
+    return true;
+  };
+
+  if (R::kEpi && warp >= 4 && warp < 8) {
+    uint32_t k = 0, seg = 0;
+    long long index = work[3];  // tile index of the segment's first tile
+    while (walk.next(P, g)) {
+      k += g.t1 - g.t0;
+      if (!finish(warp & 3, 2, g, seg, k - 1, index, (int)threadIdx.x - 128)) break;
+      index += g.t1 - g.t0;
+      ++seg;
+    }
+  } else if (warp >= R::kRows) {
+    // ---- rows: warp w of a group brings rows kTileRows * w .. of its group's tiles
+    const int grp = (warp - R::kRows) / R::kGroupWarps, w = (warp - R::kRows) % R::kGroupWarps;
+    const uint8_t* base = (const uint8_t*)(P.c.paged ? P.c.cache.latent : P.c.kv);
     uint32_t k = 0;
     int pending = -1;  // a stage whose copies were issued and not yet handed over
     bool ok = true;
-    auto hand_over = [&](int st) {  // this thread's copies have landed
+    // visible row v: the entry's row in the cache, or -1 past the last one (and for a page outside the
+    // cache)
+    auto entry = [&](const Seen& sn, int v) -> int {
+      if (v >= sn.cnt) return -1;
+      const int j = v < P.sinks ? v : v + sn.jump;
+      if (!P.c.paged) return sn.b * P.c.kv_rows + j;
+      const int ps = P.c.cache.page_size, pg = (int)((uint32_t)j / (uint32_t)ps);
+      const int page = __ldg(P.c.page_table + (long long)sn.b * P.c.max_pages + pg);
+      if (page >= 0 && page < P.c.cache.pages) return page * ps + (j - pg * ps);
+      atomicOr(P.flag, 2);
+      return -1;
+    };
+    auto hand_over = [&](int st) {  // this warp's rows have landed
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&c_full[st]);
     };
     while (ok && walk.next(P, g)) {
-      for (long long t = g.t0; t < g.t1; ++t, ++k) {
+      for (int t = g.t0; t < g.t1; ++t, ++k) {
         if ((int)(k & 1) != grp) continue;
+#ifdef CSA_DEBUG_BOUNDS
+        if (P.test_stall && walk.left == 0 && t + 1 == g.t1) break;  // test of the time-out path
+#endif
         const int st = (int)(k % (uint32_t)nst);
-        // lane r of the warp resolves its row r: the entry's row in the cache, or -1
-        long long row = -1;
-        const long long v = t * kTile + kRows * w + (lane % kRows);
-        if (v < g.s.cnt) {
-          const long long j = v < P.sinks ? v : v + g.s.jump;
-          if (P.c.paged) {
-            const uint32_t ps = (uint32_t)P.c.cache.page_size, pg = (uint32_t)j / ps;
-            const int page = __ldg(P.c.page_table + (long long)g.s.b * P.c.max_pages + pg);
-            if (page >= 0 && page < P.c.cache.pages)
-              row = (long long)page * ps + ((uint32_t)j - pg * ps);
-            else
-              atomicOr(P.flag, 2);
-          } else {
-            row = (long long)g.s.b * P.c.kv_rows + j;
-          }
-        }
+        // lane r resolves the warp's row r (and r + 32 of 64)
+        const int v = t * kTile + R::kTileRows * w + (lane & (R::kTileRows - 1) & 31);
+        const int row = entry(g.s, v), row2 = R::kTileRows == 64 ? entry(g.s, v + 32) : -1;
         const uint32_t dst = smem_addr(sC) + st * stage_bytes;
+        const uint32_t par = ((k / nst) & 1) ^ 1;  // of the stage's previous use
         if constexpr (kFp4) {
-          // units of 32 codes and two scales; loaded before the stage is free
+          // codes, expanded into the bf16 operand: units of 32 codes and two scales (eight rows of four
+          // units at a time, so that the swizzled stores hit every bank once), loaded before the
+          // stage is free
           uint4 code[8];
           uint32_t sc[8];
-          const int upr = D / 32;
+          const uint32_t upr = D / 32;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (i >= chunks) break;
-            const uint32_t x = lane + 32 * i, r = __umulhi(x, P.unit_magic), u = x - r * upr;
-            const long long rr = __shfl_sync(0xffffffffu, row, (int)r);
+            const uint32_t x = (lane >> 3) + 4 * i, hi = __umulhi(x, P.unit_magic), u = x - hi * upr;
+            const int rr = __shfl_sync(0xffffffffu, row, 8 * hi + (lane & 7));
             code[i] = make_uint4(0, 0, 0, 0);
             sc[i] = 0;
             if (rr >= 0) {
-              code[i] = __ldg(reinterpret_cast<const uint4*>(P.c.cache.codes + rr * (D / 2)) + u);
-              sc[i] = __ldg(reinterpret_cast<const uint16_t*>(P.c.cache.scales + rr * (D / 16)) + u);
+              code[i] = __ldg(reinterpret_cast<const uint4*>(P.c.cache.codes + (size_t)rr * (D / 2)) + u);
+              sc[i] = __ldg(reinterpret_cast<const uint16_t*>(P.c.cache.scales + (size_t)rr * (D / 16)) + u);
             }
           }
-          if (k >= (uint32_t)nst && !mbar_wait(&c_empty[st], ((k / nst) & 1) ^ 1, abort_flag)) {
+          if (k >= (uint32_t)nst && !mbar_wait(&c_empty[st], par, abort_flag, kWait)) ok = false;
+          if (__any_sync(0xffffffffu, !ok)) {
             ok = false;
             break;
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (i >= chunks) break;
-            const uint32_t x = lane + 32 * i, rw = __umulhi(x, P.unit_magic), u = x - rw * upr, r = kRows * w + rw;
+            const uint32_t x = (lane >> 3) + 4 * i, hi = __umulhi(x, P.unit_magic), u = x - hi * upr;
+            const uint32_t r = R::kTileRows * w + 8 * hi + (lane & 7);
             const uint32_t at = dst + (u >> 1) * kChunkBytes + r * 128;
             const uint32_t word[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-            uint32_t s2[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float s = e4m3_value((sc[i] >> (8 * h)) & 255u);
-              s2[h] = bf16x2(s, s);
-            }
+            const float s0 = e4m3_value(sc[i] & 255u), s1 = e4m3_value(sc[i] >> 8);
+            const uint32_t s2[2] = {bf16x2(s0, s0), bf16x2(s1, s1)};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const uint4 d = dequant8(word[q], s2[q >> 1]);
@@ -455,27 +596,33 @@ __global__ void __launch_bounds__(attn_threads<kFp4>(), kCtas)
           hand_over(st);
         } else {
           if (k >= (uint32_t)nst) {
-            const uint32_t par = ((k / nst) & 1) ^ 1;
             if (pending >= 0 && !mbar_test(&c_empty[st], par)) {
               cp_wait<0>();
               hand_over(pending);
               pending = -1;
             }
-            if (!mbar_wait(&c_empty[st], par, abort_flag)) {
-              ok = false;
-              break;
-            }
+            if (!mbar_wait(&c_empty[st], par, abort_flag, kWait)) ok = false;
           }
-          // 16-byte units of a row over the lanes (two or four narrow rows at a time)
-          const int units = D / 8, lpr = min(32, units), rpi = units <= 16 ? 32 / units : 1;
-          const int sub = rpi > 1 ? lane / lpr : 0, u0 = rpi > 1 ? lane % lpr : lane;
-          for (int r0 = 0; r0 < kRows; r0 += rpi) {
-            const int rw = r0 + sub, r = kRows * w + rw;
-            const long long rr = __shfl_sync(0xffffffffu, row, rw);
-            const uint8_t* src = (const uint8_t*)(base + (rr < 0 ? 0 : rr) * D);
-            for (int u = u0; u < units; u += 32)
-              cp_async16(dst + (u >> 3) * kChunkBytes + r * 128 + (((u & 7) ^ (r & 7)) << 4), src + u * 16,
-                         rr < 0 ? 0u : 16u);
+          if (__any_sync(0xffffffffu, !ok)) {
+            ok = false;
+            break;
+          }
+          // 16-byte units of the rows in order, 32 at a time
+          const uint32_t units = D / 8, step = 32u / units, rem = 32u - step * units;
+          uint32_t rw = (uint32_t)lane / units, u = lane - rw * units;
+          const int n = R::kTileRows * (int)units / 32;  // a multiple of 8
+#pragma unroll 8
+          for (int i = 0; i < n; ++i) {
+            int rr = __shfl_sync(0xffffffffu, row, rw & 31);
+            if (R::kTileRows == 64) {
+              const int r2 = __shfl_sync(0xffffffffu, row2, rw & 31);
+              rr = rw < 32 ? rr : r2;
+            }
+            const uint32_t r = R::kTileRows * w + rw;
+            cp_async16(dst + (u >> 3) * kChunkBytes + r * 128 + (((u ^ r) & 7) << 4),
+                       base + (size_t)(uint32_t)max(rr, 0) * (2 * D) + u * 16, rr < 0 ? 0u : 16u);
+            rw += step, u += rem;
+            if (u >= units) u -= units, ++rw;
           }
           cp_commit();
           if (nst == 2) {
@@ -495,112 +642,189 @@ __global__ void __launch_bounds__(attn_threads<kFp4>(), kCtas)
       cp_wait<0>();
       if (pending >= 0) hand_over(pending);
     }
-  } else if (warp == kQWarp) {
-    // ---- queries: 64 rows of [tokens * H][D] from the item's first head (rows past its heads are
-    // other tokens' or zeros: columns that nothing reads)
+  } else if (warp == R::kQ) {
+    // ---- queries: 64 rows of [B * N * H][D] from the item's first (rows past its last are other
+    // sequences' or zeros: columns that nothing reads).  The next item's are asked into L2 ahead.
     if (lane == 0) {
       int n = 0;
-      while (walk.next(P, g)) {
-        if (n > 0 && !mbar_wait(q_empty, (n - 1) & 1, abort_flag)) break;
+      bool more = walk.next(P, g);
+      while (more) {
+        const int row = g.s.b * P.c.N * P.H + g.s.f0;
+        if (n > 0 && !mbar_wait(q_empty, (n - 1) & 1, abort_flag, kWait)) break;
         mbar_arrive_expect_tx(q_full, chunks * kChunkBytes);
-        const int row = (int)(g.tok * P.H + g.hb * kHeads);
         for (int c = 0; c < chunks; ++c) tma_load_2d(sQ + c * kChunkBytes, &map_q, c * 64, row, q_full);
         *q_loads = ++n;
+        if ((more = walk.next(P, g)))
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(P.c.q + ((size_t)g.s.b * P.c.N * P.H + g.s.f0) * D),
+                       "r"(g.s.cols * D * 2)
+                       : "memory");
       }
     }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      const uint32_t idesc_s = idesc_bf16(64, kHeads), idesc_o = idesc_bf16(128, kHeads) | kTransposed,
-                     idesc_o64 = idesc_bf16(64, kHeads) | kTransposed;
-      const uint32_t q0 = smem_addr(sQ), c0 = smem_addr(sC), p0 = smem_addr(sP);
-      uint32_t k = 0, seg = 0;
-      bool ok = true;
-      auto scores = [&](uint32_t kk, bool last) {
-        const int st = (int)(kk % (uint32_t)nst);
-        if (!mbar_wait(&c_full[st], (kk / nst) & 1, abort_flag)) return false;
-        tc_fence_after();
-        const uint32_t d = tmem + oc + (kk & 1) * kHeads, c = c0 + st * stage_bytes;
-        for (int x = 0; x < chunks; ++x)
-          for (int y = 0; y < 4; ++y)
-            mma_bf16(d, sw128_desc(c + x * kChunkBytes + y * 32, 16), sw128_desc(q0 + x * kChunkBytes + y * 32, 16),
-                     idesc_s, x | y ? 1u : 0u);
-        mma_commit(&s_full[kk & 1]);
-        if (last) mma_commit(q_empty);
-        return true;
-      };
-      auto values = [&](uint32_t kk, bool first) {
-        if (!mbar_wait(&p_full[kk & 1], (kk >> 1) & 1, abort_flag)) return false;
-        if (first && seg > 0 && !mbar_wait(o_empty, (seg - 1) & 1, abort_flag)) return false;
-        tc_fence_after();
-        const int st = (int)(kk % (uint32_t)nst);
-        const uint32_t c = c0 + st * stage_bytes, p = p0 + (kk & 1) * kPBytes;
-        for (int x = 0; x < chunks; x += 2)
-          for (int y = 0; y < 4; ++y)
-            mma_bf16(tmem + (x >> 1) * kHeads, sw128_desc(c + x * kChunkBytes + y * 2048, kChunkBytes),
-                     sw128_desc(p + y * 2048, kChunkBytes), x + 1 < chunks ? idesc_o : idesc_o64, !first || y ? 1u : 0u);
-        mma_commit(&c_empty[st]);
-        mma_commit(&pv_done[kk & 1]);
-        return true;
-      };
-      while (ok && walk.next(P, g)) {
-        if (!(ok = mbar_wait(q_full, seg & 1, abort_flag))) break;
-        const long long n = g.t1 - g.t0;
-        ok = scores(k, n == 1);
-        for (long long t = 0; ok && t < n; ++t, ++k) {
-          // the next tile's scores go ahead of this tile's values, unless its rows are still on
-          // their way when this tile's weights are ready
-          bool ahead = t + 1 < n;
-          for (int spin = 0; ahead && !mbar_test(&c_full[(k + 1) % (uint32_t)nst], ((k + 1) / nst) & 1); ++spin)
-            ahead = spin < kSpins && !mbar_test(&p_full[k & 1], (k >> 1) & 1);
-          if (ahead) ok = scores(k + 1, t + 2 == n);
-          ok = ok && values(k, t == 0);
-          if (!ahead && t + 1 < n) ok = ok && scores(k + 1, t + 2 == n);
+  } else if (warp == R::kMma) {
+    // ---- MMAs: the whole warp runs the loop, one elected lane issues
+    const bool leader = elect_one();
+    const uint32_t idesc_s = idesc_bf16(64, kCols), idesc_o = idesc_bf16(128, kCols) | kTransposed,
+                   idesc_o64 = idesc_bf16(64, kCols) | kTransposed;
+    const uint32_t c0 = smem_addr(sC), p0 = smem_addr(sP);
+    const uint64_t qd = sw128_desc(smem_addr(sQ), 16);
+    uint32_t k = 0, seg = 0;
+    bool ok = true;
+    auto scores = [&](uint32_t kk, bool last) {
+      const uint32_t st = __shfl_sync(0xffffffffu, kk % (uint32_t)nst, 0), buf = __shfl_sync(0xffffffffu, kk & 1, 0);
+      if (!mbar_wait(&c_full[st], (kk / nst) & 1, abort_flag, kWait)) return false;
+      tc_fence_after();
+      const uint32_t d = tmem + oc + buf * kCols;
+      uint64_t a = sw128_desc(c0 + st * stage_bytes, 16), b = qd;  // addresses in units of 16 bytes
+      for (int x = 0; x < chunks; ++x, a += kChunkBytes / 16, b += kChunkBytes / 16)
+        if (leader) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) mma_bf16(d, a + 2 * y, b + 2 * y, idesc_s, x | y ? 1u : 0u);
         }
-        ++seg;
+      if (leader) {
+        mma_commit(&s_full[buf]);
+        if (last) mma_commit(q_empty);
       }
+      return true;
+    };
+    auto values = [&](uint32_t kk, bool first) {
+      const uint32_t st = __shfl_sync(0xffffffffu, kk % (uint32_t)nst, 0), buf = __shfl_sync(0xffffffffu, kk & 1, 0);
+      if (!mbar_wait(&p_full[buf], (kk >> 1) & 1, abort_flag, kWait)) return false;
+      if (first && seg > 0 && !mbar_wait(o_empty, (seg - 1) & 1, abort_flag, kWait)) return false;
+      tc_fence_after();
+      uint64_t a = sw128_desc(c0 + st * stage_bytes, kChunkBytes);
+      const uint64_t b = sw128_desc(p0 + buf * kPBytes, kChunkBytes);
+      for (int x = 0; x < chunks; x += 2, a += 2 * kChunkBytes / 16)
+        if (leader) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            mma_bf16(tmem + (x >> 1) * kCols, a + 128 * y, b + 128 * y, x + 1 < chunks ? idesc_o : idesc_o64,
+                     !first || y ? 1u : 0u);
+        }
+      if (leader) {
+        mma_commit(&c_empty[st]);
+        mma_commit(&pv_done[buf]);
+      }
+      return true;
+    };
+    while (ok && walk.next(P, g)) {
+      ok = mbar_wait(q_full, seg & 1, abort_flag, kWait);
+      const int n = g.t1 - g.t0;
+      ok = ok && scores(k, n == 1);
+      for (int t = 0; ok && t < n; ++t, ++k) {
+        // the next tile's scores go ahead of this tile's values, unless its rows are still on
+        // their way when this tile's weights are ready
+        bool ahead = t + 1 < n;
+        for (int spin = 0; ahead && !mbar_test(&c_full[(k + 1) % (uint32_t)nst], ((k + 1) / nst) & 1); ++spin)
+          ahead = spin < kSpins && !mbar_test(&p_full[k & 1], (k >> 1) & 1);
+        ahead = __all_sync(0xffffffffu, ahead);
+        if (ahead) ok = scores(k + 1, t + 2 == n);
+        ok = ok && values(k, t == 0);
+        if (!ahead && t + 1 < n) ok = ok && scores(k + 1, t + 2 == n);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      ++seg;
     }
   } else {
-    // ---- softmax and epilogue
+    // ---- softmax
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     const int c2 = 2 * (lane & 3);
     const float sl = P.scale_log2;
     uint32_t k = 0, seg = 0;
-    long long index = work[4];  // tile index of the segment's first tile
+    long long index = work[3];
     bool ok = true;
     while (ok && walk.next(P, g)) {
       float m[16], l[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) m[i] = kFloor, l[i] = 0.0f;
-      for (long long t = g.t0; t < g.t1; ++t, ++k) {
-        ok = mbar_wait(&s_full[k & 1], (k >> 1) & 1, abort_flag);
+      const bool several = g.s.tlo != g.s.thi;  // tokens: their rows differ
+      if (several) {
+        if (threadIdx.x < kCols) colt[threadIdx.x] = min(g.s.thi, P.c.start + (g.s.f0 + (int)threadIdx.x) / P.H);
+        group_sync(1);
+      }
+      for (int t = g.t0; t < g.t1; ++t, ++k) {
+        ok = mbar_wait(&s_full[k & 1], (k >> 1) & 1, abort_flag, kWait);
         // the weights buffer is free once the tile two before has been used
-        if (ok && k >= 2) ok = mbar_wait(&pv_done[k & 1], ((k >> 1) & 1) ^ 1, abort_flag);
+        if (ok && k >= 2) ok = mbar_wait(&pv_done[k & 1], ((k >> 1) & 1) ^ 1, abort_flag, kWait);
         tc_fence_after();
         uint32_t raw[32];
-        tmem_ld_frag(tmem + oc + (k & 1) * kHeads + lanes, raw);
+        tmem_ld_frag(tmem + oc + (k & 1) * kCols + lanes, raw);
         float x[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(raw[i]);
-        if ((t + 1) * kTile > g.s.cnt) {  // rows past the last one
-          const long long v = t * kTile + 16 * warp + (lane >> 2);
+        const int v0 = t * kTile, v1 = min(v0 + kTile, g.s.cnt), v = v0 + 16 * warp + (lane >> 2);
+        bool renew = t == g.t0 || !ok;
+        uint32_t spoilt = 0;  // bits 0, 1: this thread's rows hold a NaN or infinity that a token must not see
+        if (several) {
+          // rows that only some of the item's tokens see
+          const int first = max(v0, P.sinks);
+          if ((v1 - 1 < P.sinks ? v1 - 1 : v1 - 1 + g.s.jump) > g.s.tlo ||
+              (P.window && first < v1 && first + g.s.jump <= g.s.thi - P.window)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int vv = v + 8 * h, j = vv < P.sinks ? vv : vv + g.s.jump;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int2 tc = *reinterpret_cast<const int2*>(colt + 8 * i + c2);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int tt = e ? tc.y : tc.x;
+                  if (j > tt || (P.window && j >= P.sinks && j <= tt - P.window)) {
+                    if (!(fabsf(x[4 * i + 2 * h + e]) < INFINITY)) spoilt |= 1u << h;
+                    x[4 * i + 2 * h + e] = -INFINITY;
+                  }
+                }
+              }
+              if (vv >= g.s.cnt) spoilt &= ~(1u << h);
+            }
+            renew = renew || spoilt;
+          }
+        }
+        if (v0 + kTile > g.s.cnt) {  // rows past the last one
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (v >= g.s.cnt) x[4 * i] = x[4 * i + 1] = -INFINITY;
             if (v + 8 >= g.s.cnt) x[4 * i + 2] = x[4 * i + 3] = -INFINITY;
           }
         }
-        bool renew = t == g.t0 || !ok;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             renew = renew || fmaf(fmaxf(x[4 * i + e], x[4 * i + 2 + e]), sl, -m[2 * i + e]) > kStep;
-        if (soft_or(renew)) {
-          if (soft_or(!ok)) {
+        if (group_or(1, renew)) {
+          if (group_or(1, !ok)) {
             ok = false;
             break;
           }
-          float top[16];
+          if (several) {
+            // a row that really holds a NaN or infinity is cleared, so that the weight 0 of the tokens
+            // that do not see it makes 0; those that do get a NaN from its score
+            spoilt |= __shfl_xor_sync(0xffffffffu, spoilt, 1);
+            spoilt |= __shfl_xor_sync(0xffffffffu, spoilt, 2);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint8_t* at = sC + (k % (uint32_t)nst) * stage_bytes + (16 * warp + (lane >> 2) + 8 * h) * 128 + (lane & 3) * 32;
+              uint32_t bad = 0;
+              if (spoilt >> h & 1)
+                for (int c = 0; c < 8 * chunks; ++c) {
+                  const uint32_t y = *reinterpret_cast<const uint32_t*>(at + (c >> 3) * kChunkBytes + (c & 7) * 4);
+                  bad |= (y & 0x7F80u) == 0x7F80u || (y & 0x7F800000u) == 0x7F800000u;
+                }
+              bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+              bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+              if (!bad) continue;
+              const int j = v + 8 * h < P.sinks ? v + 8 * h : v + 8 * h + g.s.jump;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int tt = colt[8 * (i >> 1) + c2 + (i & 1)];
+                float& y = x[4 * (i >> 1) + 2 * h + (i & 1)];
+                if (y == -INFINITY && j <= tt && (!P.window || j < P.sinks || j > tt - P.window)) y = __int_as_float(0x7fffffff);
+              }
+              for (int c = 0; c < 8 * chunks; ++c)
+                *reinterpret_cast<uint32_t*>(at + (c >> 3) * kChunkBytes + (c & 7) * 4) = 0u;
+            }
+          }
+          float f[16];
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -608,33 +832,36 @@ __global__ void __launch_bounds__(attn_threads<kFp4>(), kCtas)
               float y = fmaxf(x[4 * i + e], x[4 * i + 2 + e]);
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
-              top[2 * i + e] = y * sl;
+              f[2 * i + e] = y * sl;
             }
           if (lane < 4) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) red[warp * 64 + 8 * (i >> 1) + c2 + (i & 1)] = top[i];
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float2*>(red + warp * 64 + 8 * i + c2) = make_float2(f[2 * i], f[2 * i + 1]);
           }
-          soft_sync();
-          float f[16];
+          group_sync(1);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float y = m[i];
+          for (int i = 0; i < 8; ++i) {
+            float2 y = make_float2(m[2 * i], m[2 * i + 1]);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) y = fmaxf(y, red[w * 64 + 8 * (i >> 1) + c2 + (i & 1)]);
-            f[i] = ex2(m[i] - y);
-            l[i] *= f[i];
-            m[i] = y;
+            for (int w = 0; w < 4; ++w) {
+              const float2 z = *reinterpret_cast<const float2*>(red + w * 64 + 8 * i + c2);
+              y.x = fmaxf(y.x, z.x), y.y = fmaxf(y.y, z.y);
+            }
+            f[2 * i] = ex2(m[2 * i] - y.x), f[2 * i + 1] = ex2(m[2 * i + 1] - y.y);
+            l[2 * i] *= f[2 * i], l[2 * i + 1] *= f[2 * i + 1];
+            m[2 * i] = y.x, m[2 * i + 1] = y.y;
           }
           if (t > g.t0) {
-            ok = mbar_wait(&pv_done[(k & 1) ^ 1], ((k - 1) >> 1) & 1, abort_flag);
-            if (soft_or(!ok)) {
+            ok = mbar_wait(&pv_done[(k & 1) ^ 1], ((k - 1) >> 1) & 1, abort_flag, kWait);
+            if (group_or(1, !ok)) {
               ok = false;
               break;
             }
             tc_fence_after();
             for (int x2 = 0; x2 < chunks; x2 += 2)
               for (int h = 0; h < (x2 + 1 < chunks ? 2 : 1); ++h) {
-                const uint32_t at = tmem + (x2 >> 1) * kHeads + lanes + ((uint32_t)(16 * h) << 16);
+                const uint32_t at = tmem + (x2 >> 1) * kCols + lanes + ((uint32_t)(16 * h) << 16);
                 uint32_t o[32];
                 tmem_ld_frag(at, o);
 #pragma unroll
@@ -643,28 +870,25 @@ __global__ void __launch_bounds__(attn_threads<kFp4>(), kCtas)
                 tmem_st_frag(at, o);
               }
           } else {
-            soft_sync();  // `red` has been read
+            group_sync(1);  // `red` has been read
           }
         }
-        uint32_t pk[16];
+        // weights [row][64 queries] as 128-byte swizzled rows; matrices of a store: rows 0-7 and 8-15 of
+        // two groups of 8 queries
+        const uint32_t at = smem_addr(sP) + (k & 1) * kPBytes + (16 * warp + (lane & 15)) * 128;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; i += 2) {
+          uint32_t pk[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float p0 = ex2(fmaf(x[4 * i + 2 * h], sl, -m[2 * i])),
-                        p1 = ex2(fmaf(x[4 * i + 2 * h + 1], sl, -m[2 * i + 1]));
-            l[2 * i] += p0;
-            l[2 * i + 1] += p1;
-            pk[2 * i + h] = bf16x2(p0, p1);
+          for (int j = 0; j < 4; ++j) {
+            const int q = i + (j >> 1), h = j & 1;
+            const float p0 = ex2(fmaf(x[4 * q + 2 * h], sl, -m[2 * q])),
+                        p1 = ex2(fmaf(x[4 * q + 2 * h + 1], sl, -m[2 * q + 1]));
+            l[2 * q] += p0;
+            l[2 * q + 1] += p1;
+            pk[j] = bf16x2(p0, p1);
           }
-        {
-          // weights [row][64 heads] as 128-byte swizzled rows; matrices of a store: rows 0-7 and 8-15
-          // of two head groups of 8
-          const int r = 16 * warp + (lane & 15), hg = lane >> 4;
-          const uint32_t at = smem_addr(sP) + (k & 1) * kPBytes + r * 128;
-#pragma unroll
-          for (int i = 0; i < 8; i += 2)
-            stmatrix4<false>(at + (((i + hg) ^ (r & 7)) << 4), pk[2 * i], pk[2 * i + 1], pk[2 * i + 2], pk[2 * i + 3]);
+          stmatrix4<false>(at + (((i + (lane >> 4)) ^ (lane & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
         }
         fence_async_shared();
         tc_fence_before();
@@ -672,106 +896,33 @@ __global__ void __launch_bounds__(attn_threads<kFp4>(), kCtas)
         if (lane == 0) mbar_arrive(&p_full[k & 1]);
       }
       if (!ok) break;
-      // ---- the segment's end: sums over rows, then O^T
+      // the segment's end: sums over the warp's rows
 #pragma unroll
       for (int i = 0; i < 16; ++i)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+      if (R::kEpi && seg > 0) {
+        ok = mbar_wait(l_empty, (seg - 1) & 1, abort_flag, kWait);
+        if (group_or(1, !ok)) {
+          ok = false;
+          break;
+        }
+      }
       if (lane < 4) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) red[256 + warp * 64 + 8 * (i >> 1) + c2 + (i & 1)] = l[i];
-      }
-      const uint32_t kl = k - 1;
-      ok = mbar_wait(&pv_done[kl & 1], (kl >> 1) & 1, abort_flag);
-      if (soft_or(!ok)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        l[i] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) l[i] += red[256 + w * 64 + 8 * (i >> 1) + c2 + (i & 1)];
-      }
-      const bool whole = g.t0 == 0 && g.t1 == g.tiles;
-      const int heads = min(kHeads, P.H - g.hb * kHeads);
-      const long long orow = g.tok * P.H + g.hb * kHeads;  // the item's first row of out
-      if (whole) {
-        if (P.c.lse && warp == 0 && lane < 4) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int h = 8 * (i >> 1) + c2 + (i & 1);
-            if (h < heads && in_bounds(orow + h, P.toks * P.H, P.flag))
-              P.c.lse[orow + h] = l[i] == 0.0f ? -INFINITY : (m[i] + log2f(l[i])) * 0.693147180559945f;
-          }
+        for (int i = 0; i < 8; ++i) {
+          *reinterpret_cast<float2*>(fin + warp * 64 + 8 * i + c2) = make_float2(l[2 * i], l[2 * i + 1]);
+          if (warp == 0) *reinterpret_cast<float2*>(fin + 256 + 8 * i + c2) = make_float2(m[2 * i], m[2 * i + 1]);
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) l[i] = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
-        for (int x2 = 0; x2 < chunks; x2 += 2) {
-          const bool full = x2 + 1 < chunks;  // 128 features, else 64
-          for (int h = 0; h < (full ? 2 : 1); ++h) {
-            uint32_t o[32];
-            tmem_ld_frag(tmem + (x2 >> 1) * kHeads + lanes + ((uint32_t)(16 * h) << 16), o);
-            // staged as [head][128 features] (16-byte units swizzled by the head): transposed stores
-            const int du = (full ? 4 * warp + 2 * h : 2 * warp) + ((lane >> 3) & 1);
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              uint32_t v[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int q = i + (j >> 1);
-                v[j] = bf16x2(__uint_as_float(o[4 * q + 2 * (j & 1)]) * l[2 * q],
-                              __uint_as_float(o[4 * q + 2 * (j & 1) + 1]) * l[2 * q + 1]);
-              }
-              const int head = 8 * (i + (lane >> 4)) + (lane & 7);
-              stmatrix4<true>(smem_addr(sP) + head * 256 + ((du ^ (head & 7)) << 4), v[0], v[1], v[2], v[3]);
-            }
-          }
-          soft_sync();
-          const int u = lane & 15;
-          for (int h = 2 * warp + (lane >> 4); h < heads; h += 8)
-            if ((full || u < 8) && in_bounds(orow + h, P.toks * P.H, P.flag))
-              *reinterpret_cast<uint4*>(P.c.out + (orow + h) * D + x2 * 64 + u * 8) =
-                  *reinterpret_cast<const uint4*>(sP + h * 256 + ((u ^ (h & 7)) << 4));
-          soft_sync();
-        }
+      }
+      if constexpr (R::kEpi) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(l_full);
       } else {
-        // a piece: slot 0 of the CTA for its first segment's, 1 for its last's (a first piece)
-        const int slot = 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0);
-        if (warp == 0 && lane < 4) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            P.part_ml[slot * kHeads + 8 * (i >> 1) + c2 + (i & 1)] = make_float2(m[i], l[i]);
-        }
-        float* dst = P.part + (size_t)slot * kHeads * D;
-        for (int x2 = 0; x2 < chunks; x2 += 2) {
-          const bool full = x2 + 1 < chunks;
-          const int d = x2 * 64 + (full ? 32 * warp + lane : 16 * warp + lane);
-          for (int hh = 0; hh < kHeads; hh += 32) {
-            uint32_t o[32];
-            tmem_ld32(tmem + (x2 >> 1) * kHeads + hh + lanes, o);
-            if (full || lane < 16) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (hh + i < heads) dst[(size_t)(hh + i) * D + d] = __uint_as_float(o[i]);
-            }
-          }
-        }
-        if (g.t0 == 0 && threadIdx.x == 0) {
-          // the item ends in the CTA whose share holds its last tile
-          const long long end = index + g.tiles, total = work[6], ctas = work[7];
-          long long j = (end * ctas - 1) / total;
-          while (total * (j + 1) / ctas < end) ++j;
-          while (total * j / ctas >= end) --j;
-          P.record[blockIdx.x] = make_int2((int)(g.tok * P.hblocks + g.hb), (int)(j - blockIdx.x) + 1);
-        }
-        soft_sync();  // `red` has been read before the next segment writes it
+        group_sync(1);
+        ok = finish(warp, 1, g, seg, k - 1, index, (int)threadIdx.x);
+        index += g.t1 - g.t0;
       }
-      index += g.t1 - g.t0;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(o_empty);
       ++seg;
     }
   }
@@ -780,98 +931,105 @@ __global__ void __launch_bounds__(attn_threads<kFp4>(), kCtas)
   __syncthreads();
   if (*abort_flag) {
     if (threadIdx.x == 0) atomicOr(P.flag, 4);
-    if (warp == kQWarp && lane == 0 && *q_loads > 0) mbar_wait_bounded(q_full, (*q_loads - 1) & 1);
-    if (warp == kMmaWarp && lane == 0) {
+    if (warp == R::kQ && lane == 0 && *q_loads > 0) mbar_wait_bounded(q_full, (*q_loads - 1) & 1);
+    if (warp == R::kMma && elect_one()) {  // the lane that issued them
       mma_commit(mma_done);
       mbar_wait_bounded(mma_done, 0);
     }
     __syncthreads();
   }
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, tmem_cols);
+  if (warp == R::kMma) tmem_dealloc(tmem, tmem_cols);
 }
 
-// ---- pieces of split items joined: one CTA per (record, head).
+// ---- pieces of split items joined: one CTA per record and 16 features (a warp's share of a fragment
+// load), a thread per four values of a piece.
 //   M = max m_p;  out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p
-// The pieces are added in order by each of the CTA's thread rows (a row covers the D features) and
-// the rows' sums in order after that: the result does not depend on timing.
-constexpr int kJoinThreads = 256, kMaxPieces = 1024;
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams P) {
-  __shared__ float w[kMaxPieces];
-  __shared__ float red[16];
-  __shared__ float4 acc[kJoinThreads];
+// The pieces are added in order by each of blockDim.y groups of threads and the groups' sums in order
+// after that: the result does not depend on timing.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(1024) attention_join_kernel(const AttnParams P) {
+  __shared__ float4 acc[4][kJoinThreads];
+  __shared__ __align__(16) uint16_t tile[kCols][16];
   griddep_wait();
   const int2 rec = P.record[blockIdx.x];
-  const int n = rec.y, h = blockIdx.y;
   if (rec.x < 0) return;
-  const long long tok = rec.x / P.hblocks;
-  const int hb = rec.x % P.hblocks, head = hb * kHeads + h;
-  if (head >= P.H) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = rec.y, x = blockIdx.y >> 2, w = blockIdx.y & 3, i = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = threadIdx.y, groups = blockDim.y, q = 8 * i + 2 * (lane & 3);
+  const Seen s = seen_rows(P, rec.x);
   auto slot = [&](int p) { return 2 * ((int)blockIdx.x + p) + (p == 0 ? 1 : 0); };
-  float top = kFloor;
-  for (int p = threadIdx.x; p < n; p += kJoinThreads) top = fmaxf(top, P.part_ml[slot(p) * kHeads + h].x);
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) red[warp] = top;
-  __syncthreads();
-  for (int i = 0; i < kJoinThreads / 32; ++i) top = fmaxf(top, red[i]);
-  float sum = 0.0f;
-  for (int p = threadIdx.x; p < n; p += kJoinThreads) {
-    const float2 ml = P.part_ml[slot(p) * kHeads + h];
-    w[p] = ex2(ml.x - top);
-    sum += ml.y * w[p];
-  }
-  sum = warp_sum(sum);
-  if (lane == 0) red[8 + warp] = sum;
-  __syncthreads();
-  sum = 0.0f;
-  for (int i = 0; i < kJoinThreads / 32; ++i) sum += red[8 + i];
-  const int quads = P.D / 4, rows = kJoinThreads / quads, q = threadIdx.x % quads, r = threadIdx.x / quads;
-  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (r < rows) {
+  auto ml = [&](int p) { return *reinterpret_cast<const float4*>(P.part_ml + slot(p) * kCols + q); };
+  float2 top = make_float2(kFloor, kFloor), sum = make_float2(0.0f, 0.0f);
 #pragma unroll 4
-    for (int p = r; p < n; p += rows) {
-      const float4 o = reinterpret_cast<const float4*>(P.part + ((size_t)slot(p) * kHeads + h) * P.D)[q];
-      const float f = w[p];
-      a.x = fmaf(o.x, f, a.x), a.y = fmaf(o.y, f, a.y), a.z = fmaf(o.z, f, a.z), a.w = fmaf(o.w, f, a.w);
+  for (int p = 0; p < n; ++p) {
+    const float4 y = ml(p);
+    top.x = fmaxf(top.x, y.x), top.y = fmaxf(top.y, y.z);
+  }
+#pragma unroll 4
+  for (int p = 0; p < n; ++p) {
+    const float4 y = ml(p);
+    sum.x = fmaf(y.y, ex2(y.x - top.x), sum.x), sum.y = fmaf(y.w, ex2(y.z - top.y), sum.y);
+  }
+  const float4* src = P.part + (x * 4 + w) * 256 + threadIdx.x;
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int p = grp; p < n; p += groups) {
+    const float4 y = ml(p), o = src[(size_t)slot(p) * (kCols * P.D / 4)];
+    const float f0 = ex2(y.x - top.x), f1 = ex2(y.z - top.y);
+    a.x = fmaf(o.x, f0, a.x), a.y = fmaf(o.y, f1, a.y), a.z = fmaf(o.z, f0, a.z), a.w = fmaf(o.w, f1, a.w);
+  }
+  if (groups > 1) {
+    acc[grp][threadIdx.x] = a;
+    __syncthreads();
+    if (grp == 0)
+      for (int r = 1; r < groups; ++r) {
+        const float4 o = acc[r][threadIdx.x];
+        a.x += o.x, a.y += o.y, a.z += o.z, a.w += o.w;
+      }
+  }
+  const long long orow = (long long)s.b * P.c.N * P.H + s.f0, rows = (long long)P.c.B * P.c.N * P.H;
+  if (grp == 0) {
+    const float i0 = sum.x == 0.0f ? 0.0f : 1.0f / sum.x, i1 = sum.y == 0.0f ? 0.0f : 1.0f / sum.y;
+    tile[q][lane >> 2] = bf16_bits(a.x * i0), tile[q + 1][lane >> 2] = bf16_bits(a.y * i1);
+    tile[q][8 + (lane >> 2)] = bf16_bits(a.z * i0), tile[q + 1][8 + (lane >> 2)] = bf16_bits(a.w * i1);
+    if (P.c.lse && blockIdx.y == 0 && lane < 4) {
+      for (int e = 0; e < 2; ++e) {
+        const float t = e ? sum.y : sum.x;
+        if (q + e < s.cols && in_bounds(orow + q + e, rows, P.flag))
+          P.c.lse[orow + q + e] = t == 0.0f ? -INFINITY : ((e ? top.y : top.x) + log2f(t)) * 0.693147180559945f;
+      }
     }
   }
-  acc[threadIdx.x] = a;
   __syncthreads();
-  if (r != 0) return;
-  for (int i = 1; i < rows; ++i) {
-    const float4 o = acc[i * quads + q];
-    a.x += o.x, a.y += o.y, a.z += o.z, a.w += o.w;
-  }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const long long orow = tok * P.H + head;
-  if (in_bounds(orow, P.toks * P.H, P.flag)) {
-    reinterpret_cast<uint2*>(P.c.out + orow * P.D)[q] = make_uint2(bf16x2(a.x * inv, a.y * inv), bf16x2(a.z * inv, a.w * inv));
-    if (P.c.lse && q == 0) P.c.lse[orow] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
-  }
+  // features 16 w of the last 64, else 32 w + 16 h of 128
+  const int d = (x | 1) < P.D / 64 ? (x >> 1) * 128 + 32 * w + 16 * (x & 1) : x * 64 + 16 * w;
+  const int r = threadIdx.x >> 1, u = threadIdx.x & 1;
+  if (grp == 0 && r < s.cols && r < kCols && in_bounds(orow + r, rows, P.flag))
+    *reinterpret_cast<uint4*>(P.c.out + (orow + r) * P.D + d + 8 * u) = *reinterpret_cast<const uint4*>(&tile[r][8 * u]);
 }
 
 // ---- host side
 // Stages: as many tiles (a power of two, at most 8) as the shared memory takes: two CTAs an SM up
-// to D = 192 (their tensor memory is 256 columns), else one.
+// to D = 192 over latents (their tensor memory is 256 columns), else one.
 struct Shape {
   int ctas, stages, smem;
 };
 Shape attn_shape(int D, bool fp4) {
   Shape s;
   s.ctas = D <= 192 && !fp4 ? 2 : 1;
-  const int chunk = D / 64 * kChunkBytes, budget = (s.ctas == 2 ? 113 : 227) * 1024 - 1024 - kAuxBytes;
+  const int chunk = D / 64 * kChunkBytes, rest = 2 * kPBytes + 4 * kStageOut + kAuxBytes + 1024;
+  const int budget = (s.ctas == 2 ? 113 : 227) * 1024 - rest;
   s.stages = 8;
-  while (s.stages > 2 && (s.stages + 1) * chunk + 2 * kPBytes > budget) s.stages /= 2;
-  s.smem = (s.stages + 1) * chunk + 2 * kPBytes + kAuxBytes + 1024;
+  while (s.stages > 2 && (s.stages + 1) * chunk > budget) s.stages /= 2;
+  s.smem = (s.stages + 1) * chunk + rest;
   return s;
 }
+int attn_slots(int D) { return 2 * current_sm_count() * attn_shape(D, false).ctas; }
 
 }  // namespace
 
 size_t attention_workspace_bytes(int head_dim) {
-  const size_t slots = 2 * (size_t)current_sm_count() * attn_shape(head_dim, false).ctas;
-  return slots * kHeads * (head_dim * sizeof(float) + sizeof(float2)) + slots * sizeof(int2);
+  return (size_t)attn_slots(head_dim) * (kCols * (head_dim * sizeof(float) + sizeof(float2)) + sizeof(int2));
 }
 
 cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_t s) {
@@ -880,6 +1038,7 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
   const bool fp4 = call.paged && !call.cache.latent;
   const Shape sh = attn_shape(a->D, fp4);
   auto* kernel = fp4 ? attention_kernel<true, 1> : sh.ctas == 2 ? attention_kernel<false, 2> : attention_kernel<false, 1>;
+  const int threads = fp4 ? Roles<true, 1>::kThreads : sh.ctas == 2 ? Roles<false, 2>::kThreads : Roles<false, 1>::kThreads;
   static std::atomic<unsigned long long> attr{0};
   cudaError_t e = once_per_device(attr, [] {
     const int most = 227 * 1024;
@@ -889,49 +1048,54 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
     return r;
   });
   if (e != cudaSuccess) return e;
-  const int sms = current_sm_count();
-  const int slots = 2 * sms * attn_shape(a->D, false).ctas;
+  const int slots = attn_slots(a->D), most_ctas = current_sm_count() * sh.ctas;
   AttnParams P{};
   P.c = call;
   P.H = a->heads;
   P.D = a->D;
   P.window = a->window;
   P.sinks = a->sinks;
-  P.hblocks = (a->heads + kHeads - 1) / kHeads;
-  P.toks = (long long)call.B * call.N;
+  P.per = (int)(((long long)call.N * a->heads + kCols - 1) / kCols);
+  P.items = call.B * P.per;
   P.scale_log2 = (float)(a->scale * 1.4426950408889634);
   P.flag = a->dev_flag;
-  P.part = (float*)a->workspace;
-  P.part_ml = (float2*)(P.part + (size_t)slots * kHeads * a->D);
-  P.record = (int2*)(P.part_ml + (size_t)slots * kHeads);
+  P.part = (float4*)a->workspace;
+  P.part_ml = (float2*)((float*)a->workspace + (size_t)slots * kCols * a->D);
+  P.record = (int2*)(P.part_ml + (size_t)slots * kCols);
   P.stages = sh.stages;
   P.unit_magic = (uint32_t)((0x100000000ull + a->D / 32 - 1) / (a->D / 32));
-  // the longest visible range that this call can have decides whether items may be cut
+#ifdef CSA_DEBUG_BOUNDS
+  P.test_stall = getenv("CSA_TEST_STALL_LAST_STAGE") != nullptr;
+  P.wait_ns = P.test_stall ? 200000000ull : kWaitNs;
+#endif
+  // the longest range of rows that this call can have decides whether items may be cut
   long long most = call.paged ? (long long)call.max_pages * call.cache.page_size : (long long)call.start + call.N;
-  if (a->window && most > (long long)a->window + a->sinks) most = (long long)a->window + a->sinks;
+  const long long window = (long long)a->window + a->sinks + kCols / a->heads;
+  if (a->window && most > window) most = window;
   P.split = most > (long long)kJoinTiles * kTile;
-  const long long tiles = P.toks * P.hblocks * ((most + kTile - 1) / kTile > 0 ? (most + kTile - 1) / kTile : 1);
-  const int grid = (int)(tiles < (long long)sms * sh.ctas ? tiles : (long long)sms * sh.ctas);
+  const long long tiles = P.items * (most > kTile ? (most + kTile - 1) / kTile : 1);
+  const int grid = (int)(tiles < most_ctas ? tiles : most_ctas);
   CUtensorMap mq;
   {
-    cuuint64_t dims[2] = {(cuuint64_t)a->D, (cuuint64_t)(P.toks * a->heads)};
+    cuuint64_t dims[2] = {(cuuint64_t)a->D, (cuuint64_t)call.B * call.N * a->heads};
     cuuint64_t strides[1] = {(cuuint64_t)a->D * 2};
-    cuuint32_t box[2] = {64, kHeads};
+    cuuint32_t box[2] = {64, kCols};
     cuuint32_t es[2] = {1, 1};
     if (encode(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (void*)call.q, dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  kernel<<<grid, fp4 ? attn_threads<true>() : attn_threads<false>(), sh.smem, s>>>(mq, P);
+  kernel<<<grid, threads, sh.smem, s>>>(mq, P);
   a->launches += 1;
   if ((e = cudaGetLastError()) != cudaSuccess || !P.split) return e;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, a->heads < kHeads ? a->heads : kHeads);
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = dim3(grid, a->D / 16);
+  // few items have many pieces each: four groups of threads share them
+  cfg.blockDim = dim3(kJoinThreads, P.items * 8 <= grid ? 4 : 1);
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;

@@ -122,6 +122,8 @@ int csa_attention_prefill(csa_attention* a, const uint16_t* q, const uint16_t* k
     return fail(CSA_ERR_ARG, "%s: start_pos %d must be >= 0 and start_pos + N below 2^30", what, start_pos);
   if (kv_rows < start_pos + N)
     return fail(CSA_ERR_ARG, "%s: kv_rows %d must be at least start_pos + N = %d", what, kv_rows, start_pos + N);
+  if ((long long)B * kv_rows > 0x7ffffffeLL)
+    return fail(CSA_ERR_ARG, "%s: B * kv_rows must be below 2^31 - 1", what);
   if (!q || !kv || !out) return fail(CSA_ERR_ARG, "%s: q, kv and out are required", what);
   if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 16))
     return fail(CSA_ERR_ARG, "%s: q, kv and out must be 16-byte aligned", what);
@@ -149,6 +151,8 @@ int csa_attention_decode(csa_attention* a, const uint16_t* q, const csa_cache* c
     return fail(CSA_ERR_ARG, "%s: the cache holds %d features, the handle %d", what, cache->head_dim, a->D);
   if (!cache->latent && cache->fp4 != 1)
     return fail(CSA_ERR_ARG, "%s: codes must have e4m3 scales per 16 (fp4 = 1)", what);
+  if (cache->latent && cache->pages > 0x7ffffffeLL / cache->page_size)
+    return fail(CSA_ERR_ARG, "%s: the cache's entries must number less than 2^31 - 1", what);
   if (B < 1 || (long long)B * a->heads > 0x7fffffffLL) return fail(CSA_ERR_ARG, "%s: B (%d) must be >= 1", what, B);
   if (max_pages < 0 || (max_pages > 0 && !page_table))
     return fail(CSA_ERR_ARG, "%s: page_table is required", what);
