@@ -100,6 +100,7 @@ int csa_attention_create(int heads, int head_dim, int window, int sinks, float s
   if (e == cudaSuccess) e = cudaMalloc((void**)&a->dev_flag, sizeof(int));
   if (e == cudaSuccess) e = cudaMalloc((void**)&a->workspace, csa::attention_workspace_bytes(head_dim));
   if (e == cudaSuccess) e = cudaMemset(a->dev_flag, 0, sizeof(int));
+  if (e == cudaSuccess) e = cudaMemset(a->workspace, 0, csa::attention_workspace_bytes(head_dim));
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     cudaFree(a->dev_flag);
