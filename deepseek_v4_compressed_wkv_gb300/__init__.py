@@ -71,6 +71,8 @@ def library_path() -> str:
 def load_library(build_if_missing: bool = True):
     """Loads libcsa.so (building it first if it is missing and nvcc is available)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -45,24 +45,39 @@ constexpr int kTile = 64;                      // rows of a tile
 constexpr int kCols = 64;                      // queries of an item
 constexpr int kChunkBytes = 8192;              // 64 rows x 64 features bf16: one column of swizzled atoms
 constexpr int kPBytes = kTile * kCols * 2;     // one weights buffer
-constexpr int kStageOut = 2048;                // a warp's staging of 32 queries x 32 features bf16
+constexpr int kStageOut = 1024;                // a warp's staging of 16 queries x 32 features bf16
 constexpr int kJoinTiles = 6;   // items longer than this are split
 constexpr int kMinTiles = 4;    // a split call gives a CTA at least this many tiles
 constexpr float kStep = 16.0f;  // base-2 steps a score may pass the reference by
 constexpr float kFloor = -1e38f;  // a reference that any score passes
 constexpr int kSpins = 1 << 16;   // polls of two barriers before the MMA warp waits for one of them
-constexpr int kAuxBytes = 3584;   // barriers, flags, per-warp maxima and sums
+constexpr int kAuxBytes = 6144;   // barriers, flags, references and sums
+
+// Division of 31-bit numbers by a number known to the host: with l = ceil(log2 d) and
+// m = floor(2^(31 + l) / d) + 1, n / d = (m n) >> (31 + l) (Granlund and Montgomery, 1994).
+struct Divisor {
+  uint32_t d, m;
+  int shift;
+  Divisor(uint32_t by = 1) : d(by), shift(31) {
+    while ((1u << (shift - 31)) < by) ++shift;
+    m = (uint32_t)((1ull << shift) / by + 1);
+  }
+  __device__ __forceinline__ int of(int n) const { return (int)(((uint64_t)m * (uint32_t)n) >> shift); }
+};
 
 struct AttnParams {
   AttnCall c;
   int H, D, window, sinks;
   int per, items;    // items of a sequence, of the call
+  Divisor by_per, by_heads, by_page;
   float scale_log2;  // scale * log2(e): scores in base-2 exponents
   int* flag;
   float4* part;      // pieces: [2 * grid][64 * D / 4] f32, in the order of the fragment loads
   float2* part_ml;   // (maximum, sum) of each piece and query [2 * grid][64]
-  int2* record;      // per CTA: (item, pieces) of an item whose first piece it made, or (-1, 0)
-  int stages;
+  int2* record;      // per CTA: (item, pieces) of an item whose first piece it made, or (-1, 0); per
+                     // item with few of them: (CTA of the first piece, pieces), or (-1, 0)
+  bool few;
+  int log_stages;
   bool split;        // items may be cut (the join kernel follows); else they are drawn from `ticket`
   int* ticket;       // items drawn beyond each CTA's first; 0 between calls
 #ifdef CSA_DEBUG_BOUNDS
@@ -82,7 +97,7 @@ struct Seen {
 
 __device__ __forceinline__ Seen seen_rows(const AttnParams& P, int item) {
   Seen s;
-  s.b = item / P.per;
+  s.b = P.by_per.of(item);
   s.f0 = (item - s.b * P.per) * kCols;
   if (P.c.paged) {
     const int top = P.c.max_pages * P.c.cache.page_size, n = __ldg(P.c.lens + s.b);
@@ -91,14 +106,14 @@ __device__ __forceinline__ Seen seen_rows(const AttnParams& P, int item) {
   } else {
     const int n = P.c.lens ? min(max(__ldg(P.c.lens + s.b), 0), P.c.N) : P.c.N;
     s.cols = max(0, min(kCols, n * P.H - s.f0));
-    s.tlo = P.c.start + s.f0 / P.H;
-    s.thi = P.c.start + (s.f0 + max(s.cols, 1) - 1) / P.H;
+    s.tlo = P.c.start + P.by_heads.of(s.f0);
+    s.thi = P.c.start + P.by_heads.of(s.f0 + max(s.cols, 1) - 1);
   }
   // every token from tlo on sees the rows after thi - most and the sinks at most
-  const long long most = (long long)P.window + (s.thi - s.tlo) + P.sinks;
+  const int most = P.window + (s.thi - s.tlo) + P.sinks;
   const bool all = P.window == 0 || s.thi + 1 <= most;
-  s.cnt = all ? s.thi + 1 : (int)most;
-  s.jump = all ? 0 : s.thi + 1 - (int)most;
+  s.cnt = all ? s.thi + 1 : most;
+  s.jump = all ? 0 : s.thi + 1 - most;
   return s;
 }
 __device__ __forceinline__ int tiles_of(const Seen& s) {
@@ -109,10 +124,9 @@ __device__ __forceinline__ int tiles_of(const Seen& s) {
 struct __align__(16) Segment {
   Seen s;
   int item, t0, t1, tiles;  // tiles [t0, t1) of the item's; t1 0: no more segments
-  int pad;
-  long long index;          // tile t0's number among the call's tiles (split calls)
+  int index;                // tile t0's number among the call's tiles (split calls)
 };
-static_assert(sizeof(Segment) == 64, "a ring slot");
+static_assert(sizeof(Segment) == 48, "a ring slot");
 constexpr int kRing = 4;
 
 // ---- tensor-core helpers
@@ -200,15 +214,19 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t wait_ns) {
   return mbar_wait(bar, parity, abort_flag, wait_ns);
 }
-// A barrier of four warps (1: softmax, 2: epilogue); group_or gives every thread whether any passed
+// A barrier of some warps (1: softmax, 2: epilogue); group_or gives every thread whether any passed
 // true.
-__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+template <int kThreads = 128>
+__device__ __forceinline__ void group_sync(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
+}
+template <int kThreads = 128>
 __device__ __forceinline__ bool group_or(int id, bool p) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)p), "r"(id)
+      : "r"((uint32_t)p), "r"(id), "n"(kThreads)
       : "memory");
   return r != 0;
 }
@@ -232,22 +250,23 @@ __device__ __forceinline__ void cp_wait() {
 // a magnitude's bf16 pattern (0, .5, 1, 1.5, 2, 3, 4, 6) are looked up by byte permutation; products
 // of 2 and 4 significant bits are exact in bf16.
 __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t scale2) {
-  const uint32_t m0 = w & 0x77777777u, m1 = m0 >> 16;
-  const uint32_t h0 = __byte_perm(0x3F3F3F00u, 0x40404040u, m0), h1 = __byte_perm(0x3F3F3F00u, 0x40404040u, m1);
-  const uint32_t l0 = __byte_perm(0xC0800000u, 0xC0804000u, m0), l1 = __byte_perm(0xC0800000u, 0xC0804000u, m1);
-  uint32_t v[4] = {__byte_perm(l0, h0, 0x5140), __byte_perm(l0, h0, 0x7362), __byte_perm(l1, h1, 0x5140),
-                   __byte_perm(l1, h1, 0x7362)};
+  const uint32_t m = w & 0x77777777u;
+  uint32_t v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // the signs are bits 3 and 7 of byte i: to bits 15 and 31
-    const uint32_t s = ((w >> (8 * i)) & 0x88u) * 0x01001000u;
-    v[i] |= s & 0x80008000u;
-    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(scale2));
+  for (int h = 0; h < 2; ++h) {  // four codes each
+    const uint32_t sel = m >> (16 * h), lo = __byte_perm(0xC0800000u, 0xC0804000u, sel);
+    // high bytes with the codes' signs, bits 3 and 7 of the two bytes that hold them
+    const uint32_t b = __byte_perm(w, 0u, h ? 0x3322 : 0x1100);
+    const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, sel) | (((b & 0xFF00FF00u) | ((b << 4) & 0x00FF00FFu)) & 0x80808080u);
+    v[2 * h] = __byte_perm(lo, hi, 0x5140);
+    v[2 * h + 1] = __byte_perm(lo, hi, 0x7362);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(scale2));
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// ---- the kernel's warps: 0-3 softmax (TMEM lane quarter = warp); with one CTA an SM 4-7 the
+// ---- the kernel's warps: 0-3 softmax (TMEM lane quarter = warp); with one CTA an SM 4-11 the
 // epilogue, which reads O^T while the softmax warps go on with the next item (up to D = 192 two CTAs
 // share an SM instead, whose softmax warps read their own O^T); then one that issues the MMAs, one
 // for the queries' copies, and the rows' warps in two groups that take alternate tiles (one group's
@@ -255,7 +274,8 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t scale2) {
 template <bool kFp4, int kCtas>
 struct Roles {
   static constexpr bool kEpi = kCtas == 1;
-  static constexpr int kMma = kEpi ? 8 : 4, kQ = kMma + 1, kRows = kMma + 2;
+  static constexpr int kEpiWarps = kEpi ? 8 : 4;  // warps that read O^T
+  static constexpr int kMma = kEpi ? 4 + kEpiWarps : 4, kQ = kMma + 1, kRows = kMma + 2;
   static constexpr int kRowWarps = kCtas == 2 ? 2 : 4;
   static constexpr int kGroupWarps = kRowWarps / 2;
   static constexpr int kTileRows = kTile / kGroupWarps;  // rows of a tile a warp brings
@@ -264,18 +284,19 @@ struct Roles {
 
 template <bool kFp4, int kCtas>
 __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
-    attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ AttnParams P) {
+    attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_c,
+                     const __grid_constant__ AttnParams P) {
   using R = Roles<kFp4, kCtas>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const int D = P.D, chunks = D / 64;
-  const uint32_t nst = P.stages;
+  const uint32_t lst = P.log_stages, nst = 1u << lst;  // stages: a power of two
   const int stage_bytes = chunks * kChunkBytes;
   uint8_t* sQ = smem;
   uint8_t* sC = sQ + chunks * kChunkBytes;
   uint8_t* sP = sC + nst * stage_bytes;  // two weights buffers
-  uint8_t* sO = sP + 2 * kPBytes;        // the epilogue's staging, 2 KB a warp
-  uint8_t* aux = sO + 4 * kStageOut;
+  uint8_t* sO = sP + 2 * kPBytes;        // the epilogue's staging, 1 KB a warp
+  uint8_t* aux = sO + 8 * kStageOut;
   uint64_t* c_full = (uint64_t*)aux;  // [8] a stage's rows have landed
   uint64_t* c_empty = c_full + 8;     // [8] a stage's products are done
   uint64_t* s_full = c_empty + 8;     // [2] scores ready
@@ -285,19 +306,19 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
   uint64_t* g_empty = g_full + kRing; // [4] and has been read by every role
   uint64_t* q_full = g_empty + kRing;
   uint64_t* q_empty = q_full + 1;
-  uint64_t* o_empty = q_empty + 1;    // O^T has been read
-  uint64_t* l_full = o_empty + 1;     // the item's references and sums are in `fin`
+  uint64_t* o_empty = q_empty + 1;    // [4] O^T's block of 128 features has been read
+  uint64_t* l_full = o_empty + 4;     // the item's references and sums are in `fin`
   uint64_t* l_empty = l_full + 1;     // and have been read
   uint64_t* mma_done = l_empty + 1;   // clean-up after an abort
   uint32_t* tmem_slot = (uint32_t*)(mma_done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   Segment* ring = (Segment*)(aux + 384);
-  long long* work = (long long*)(aux + 640);  // split calls: first item, tile, tiles, tile index, end, total, CTAs
-  float* red = (float*)(aux + 704);   // [4][64] per-warp maxima; the scan's sums before
-  float* fin = red + 256;             // [4][64] per-warp sums, [64] references
-  float* inv = fin + 320;             // [64] 1 / sum
+  int* work = (int*)(aux + 640);  // split calls: first item, tile, tiles, tile index, end, tiles of a share, shares with one more
+  float* red = (float*)(aux + 704);   // [2][64] references, factors; the scan's sums before
+  float* fin = red + 128;             // [16][64] sums over rows, [64] references
+  float* inv = fin + 1088;            // [64] 1 / sum
   int* colt = (int*)(inv + 64);       // [64] the queries' positions
-  static_assert(704 + (256 + 320 + 64 + 64) * 4 <= kAuxBytes, "aux region");
+  static_assert(704 + (128 + 1088 + 64 + 64) * 4 <= kAuxBytes, "aux region");
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 #ifdef CSA_DEBUG_BOUNDS
@@ -325,9 +346,9 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    mbar_init(o_empty, 4);
+    for (int i = 0; i < 4; ++i) mbar_init(&o_empty[i], R::kEpiWarps);
     mbar_init(l_full, 4);
-    mbar_init(l_empty, 4);
+    mbar_init(l_empty, R::kEpiWarps);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -350,47 +371,49 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     // contiguous items) and finds its own first one
     const int per = (P.items + R::kThreads - 1) / R::kThreads, lo = min(P.items, per * (int)threadIdx.x),
               hi = min(P.items, lo + per);
-    long long sum = 0;
-    int top = 0;
+    int sum = 0, top = 0, all = 0;  // (the host has made sure that the call's tiles fit)
 #pragma unroll 1
     for (int i = lo; i < hi; ++i) {
       const int n = tiles_of(seen_rows(P, i));
       sum += n;
       top = max(top, n);
     }
-    long long pre = sum;
+    int pre = sum;
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, pre, o);
+      const int y = __shfl_up_sync(0xffffffffu, pre, o);
       if (lane >= o) pre += y;
       top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     }
-    long long* ws = (long long*)red;  // [warp] sums, then [warp] maxima
+    int* ws = (int*)red;  // [warp] sums, then [warp] maxima
     if (lane == 31) ws[warp] = pre, ws[32 + warp] = top;
     __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < R::kThreads / 32; ++w) {
-      if (w < warp) before += ws[w];
-      total += ws[w];
-      top = max(top, (int)ws[32 + w]);
+    {
+      const int y = lane < R::kThreads / 32 ? ws[lane] : 0;
+      top = lane < R::kThreads / 32 ? ws[32 + lane] : 0;
+      pre += __reduce_add_sync(0xffffffffu, lane < warp ? y : 0) - sum;  // tiles before this thread's items
+      sum = pre + sum;                                                   // and with them
+      top = __reduce_max_sync(0xffffffffu, top);
+      all = __reduce_add_sync(0xffffffffu, y);
     }
-    pre += before - sum;  // tiles before this thread's items
+    const int total = all;
     const bool cut = top > kJoinTiles;
-    const long long ctas = cut ? min((long long)gridDim.x, max(1LL, total / kMinTiles)) : gridDim.x;
-    const long long i = blockIdx.x;
-    const long long a = i < ctas ? total * i / ctas : total, e = i < ctas ? total * (i + 1) / ctas : total;
-    if (threadIdx.x == 0) work[0] = P.items, work[1] = 0, work[3] = work[4] = total, work[5] = total, work[6] = ctas;
+    const int ctas = cut ? min((int)gridDim.x, max(1, total / kMinTiles)) : (int)gridDim.x;
+    // share i begins at each * i + min(i, more)
+    const int each = total / ctas, more = total - each * ctas, i0 = min((int)blockIdx.x, ctas), i1 = min(i0 + 1, ctas);
+    const int a = each * i0 + min(i0, more), e = each * i1 + min(i1, more);
+    if (threadIdx.x == 0) work[0] = P.items, work[1] = 0, work[3] = work[4] = total, work[5] = each, work[6] = more;
     __syncthreads();
     // the boundary x: the item it falls in or, without cutting, the first item that starts from it on
-    if ((a >= pre && a < pre + sum) || (e >= pre && e < pre + sum)) {
-      long long at = pre;
+    if ((a >= pre && a < sum) || (e >= pre && e < sum)) {
+      int at = pre;
 #pragma unroll 1
       for (int item = lo; item < hi; ++item) {
         const int n = tiles_of(seen_rows(P, item));
 #pragma unroll 1
         for (int w = 0; w < 2; ++w) {
-          const long long x = w ? e : a;
+          const int x = w ? e : a;
           if (x < at || x >= at + n) continue;
-          const int tile = (int)(x - at);
+          const int tile = x - at;
           const bool move = !cut && tile > 0;
           if (w == 0) work[0] = item + move, work[1] = move ? 0 : tile;
           work[3 + w] = move ? at + n : x;
@@ -401,7 +424,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     __syncthreads();
     if (threadIdx.x == 0) {
       work[2] = work[4] - work[3];
-      P.record[blockIdx.x] = make_int2(-1, 0);
+      if (!P.few) P.record[blockIdx.x] = make_int2(-1, 0);
     }
   }
   tc_fence_before();
@@ -414,7 +437,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
   Segment g;
   auto next = [&]() {
     const uint32_t slot = seg % kRing;
-    if (!wait(&g_full[slot], seg / kRing)) return false;
+    if (!__all_sync(0xffffffffu, wait(&g_full[slot], seg / kRing))) return false;
     g = ring[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&g_empty[slot]);
@@ -422,19 +445,26 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     return g.t1 > 0;
   };
 
-  // ---- an item's end, by the four warps that own O^T's lane quarters (w = warp % 4): the sums over
-  // rows in `fin`, O^T (complete with tile kl) scaled to out, or left as a piece.  False after an abort.
-  auto finish = [&](int w, int bar, uint32_t kl, int tid) -> bool {
+  // ---- an item's end, by the warps that read O^T's lane quarters (warp % 4; two warps of a quarter
+  // share its columns or halves): the sums over rows in `fin`, O^T (complete with tile kl) scaled to
+  // out, or left as a piece.  A block of 128 features is given back to the MMAs as soon as it has
+  // been read.  False after an abort.
+  auto finish = [&](uint32_t kl, int tid) -> bool {
+    constexpr int bar = R::kEpi ? 2 : 1, kEpiThreads = 32 * R::kEpiWarps, kTwo = R::kEpiWarps / 4;
+    const int w = warp & 3, half = tid >> 7;
     bool ok = !R::kEpi || wait(l_full, seg - 1);
     ok = ok && wait(&pv_done[kl & 1], kl >> 1);
-    if (group_or(bar, !ok)) return false;
+    if (group_or<kEpiThreads>(bar, !ok)) return false;
     tc_fence_after();
     const bool whole = g.t0 == 0 && g.t1 == g.tiles;
     // a piece: slot 0 of the CTA for its first segment's, 1 for its last's (an item's first piece)
     const int slot = 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0);
     const long long orow = (long long)g.s.b * P.c.N * P.H + g.s.f0, rows = (long long)P.c.B * P.c.N * P.H;
     if (tid < kCols) {
-      const float l = (fin[tid] + fin[64 + tid]) + (fin[128 + tid] + fin[192 + tid]), m = fin[256 + tid];
+      float l = 0.0f;
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) l += fin[64 * i + tid];
+      const float m = fin[1024 + tid];
       if (whole) {
         float r, lg;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(l));
@@ -446,103 +476,127 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         P.part_ml[slot * kCols + tid] = make_float2(m, l);
       }
     }
-    group_sync(bar);
+    group_sync<kEpiThreads>(bar);
     if (R::kEpi && lane == 0) mbar_arrive(l_empty);
+    auto give_back = [&](int block) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_empty[block]);
+    };
     const uint32_t base = tmem + ((uint32_t)(32 * w) << 16);
     if (whole) {
-      // steps of 32 queries x 16 or 32 features; the next step's loads run ahead of a step's stores
-      uint8_t* stage = sO + w * kStageOut;
-      const int u = lane & 3;
+      if (P.split && P.few && tid == 0) P.record[g.item] = make_int2(-1, 0);
+      // steps of 32 queries x 32 features (16 of a last block of 64) a warp; the next step's loads run
+      // ahead of a step's stores
+      const int steps = (chunks + 1) & ~1;  // two of a block
       uint32_t o[2][16];
-      tmem_ld_half(base, o[0]);
-      tmem_ld_half(base + (16u << 16), o[1]);
-      const int steps = (chunks + 1) & ~1;
+      tmem_ld_half(base + 32 * half, o[0]);
+      tmem_ld_half(base + 32 * half + (16u << 16), o[1]);
 #pragma unroll 1
-      for (int step = 0; step < steps; ++step) {
+      for (int step = half; step < steps; step += kTwo) {
         const int x = step & ~1, c = step & 1;
-        const bool full = x + 1 < chunks;  // 128 features: 32 a warp; else 64: 16
+        const bool full = x + 1 < chunks;
         float2 f[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) f[q] = *reinterpret_cast<const float2*>(inv + 32 * c + 8 * q + 2 * (lane & 3));
         tmem_ld_wait();
-        // to [query][32 features] by transposed stores; 16-byte units swizzled against conflicts
+        uint32_t v[2][2][4];
 #pragma unroll
-        for (int i = 0; i < 4; i += 2)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t v[4];
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const int q = i + (j >> 1);
-              v[j] = bf16x2(__uint_as_float(o[h][4 * q + 2 * (j & 1)]) * f[q].x,
-                            __uint_as_float(o[h][4 * q + 2 * (j & 1) + 1]) * f[q].y);
+              const int q = 2 * i + (j >> 1);
+              v[i][h][j] = bf16x2(__uint_as_float(o[h][4 * q + 2 * (j & 1)]) * f[q].x,
+                                  __uint_as_float(o[h][4 * q + 2 * (j & 1) + 1]) * f[q].y);
             }
-            const int r = 8 * (i + (lane >> 4)) + (lane & 7), uu = 2 * h + ((lane >> 3) & 1);
-            stmatrix4<true>(smem_addr(stage) + r * 64 + ((uu ^ ((r >> 1) & 3)) << 4), v[0], v[1], v[2], v[3]);
-          }
-        if (step + 1 < steps) {
-          const uint32_t at = base + 32 * (step + 1);  // 64 columns a block of 128 features
+        if (kTwo == 2 || c == 1) give_back(step >> 1);
+        if (step + kTwo < steps) {
+          const uint32_t at = base + 32 * (step + kTwo);  // 64 columns a block of 128 features
           tmem_ld_half(at, o[0]);
           tmem_ld_half(at + (16u << 16), o[1]);
         }
-        __syncwarp();
-        uint4 y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = (lane >> 2) + 8 * i;
-          y[i] = *reinterpret_cast<const uint4*>(stage + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
-        }
-        __syncwarp();
+        // to [query][32 features] by transposed stores, 16 queries at a time; 16-byte units swizzled
+        // against conflicts
+        uint8_t* stage = sO + (warp - (R::kEpi ? 4 : 0)) * kStageOut;
+        const int r = 8 * (lane >> 4) + (lane & 7), u = lane & 3;
         uint16_t* dst = P.c.out + (orow + 32 * c + (lane >> 2)) * D + x * 64 + w * (full ? 32 : 16) + 8 * u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int q = 32 * c + (lane >> 2) + 8 * i;
-          if ((full || u < 2) && q < g.s.cols && in_bounds(orow + q, rows, P.flag))
-            *reinterpret_cast<uint4*>(dst + (size_t)(8 * i) * D) = y[i];
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            stmatrix4<true>(smem_addr(stage) + r * 64 + (((2 * h + ((lane >> 3) & 1)) ^ ((r >> 1) & 3)) << 4), v[i][h][0],
+                            v[i][h][1], v[i][h][2], v[i][h][3]);
+          __syncwarp();
+          uint4 y[2];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int rr = (lane >> 2) + 8 * z;
+            y[z] = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((u ^ ((rr >> 1) & 3)) << 4));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int q = 32 * c + 16 * i + 8 * z + (lane >> 2);
+            if ((full || u < 2) && q < g.s.cols && in_bounds(orow + q, rows, P.flag))
+              *reinterpret_cast<uint4*>(dst + (size_t)(16 * i + 8 * z) * D) = y[z];
+          }
         }
       }
     } else {
       float4* dst = P.part + (size_t)slot * (kCols * D / 4) + w * 256 + lane;
 #pragma unroll 1
-      for (int x = 0; x < chunks; ++x) {  // half x % 2 of 16 lanes a warp of the block of 128 features
+      for (int x = half; x < ((chunks + 1) & ~1); x += kTwo) {  // half x % 2 of 16 lanes a warp of a block
+        if (x < chunks) {
         uint32_t o[32];
         tmem_ld_frag(base + (x >> 1) * kCols + ((uint32_t)(16 * (x & 1)) << 16), o);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           dst[(x * 32 + i) * 32] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+        }
+        if (kTwo == 2 || (x & 1)) give_back(x >> 1);
       }
       if (g.t0 == 0 && tid == 0) {
         // the item ends in the CTA whose share holds its last tile
-        const long long end = g.index + g.tiles, total = work[5], ctas = work[6];
-        long long j = (end * ctas - 1) / total;
-        while (total * (j + 1) / ctas < end) ++j;
-        while (total * j / ctas >= end) --j;
-        P.record[blockIdx.x] = make_int2(g.item, (int)(j - blockIdx.x) + 1);
+        const int last = g.index + g.tiles - 1, each = work[5], more = work[6], wide = more * (each + 1);
+        const int j = last < wide ? last / (each + 1) : more + (last - wide) / each;
+        const int n = j - (int)blockIdx.x + 1;
+        P.record[P.few ? g.item : blockIdx.x] = make_int2(P.few ? (int)blockIdx.x : g.item, n);
       }
     }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(o_empty);
     return true;
   };
 
   if (warp == R::kQ) {
     // ---- scheduling and queries (one lane).  A split call's segments are the CTA's share; otherwise
-    // items are drawn one at a time, the CTA's first being its own number: SMs differ in speed and
-    // padding in place.  The CTA that draws the last ticket sets the counter back.  A segment is
+    // items are drawn one at a time from the last (a prompt's longest) on, the CTA's first by its own
+    // number: SMs differ in speed, items in length and padding in place.  The CTA that draws the last
+    // ticket sets the counter back.  A segment is
     // published one ahead of its queries' copy (64 rows of [B * N * H][D] from the item's first; rows past
     // its last are other sequences' or zeros: columns that nothing reads).
     if (lane == 0) {
       const bool split = P.split;
-      int item = split ? (int)work[0] : blockIdx.x, tile = split ? (int)work[1] : 0, drawn = 0;
-      long long left = split ? work[2] : 0, index = split ? work[3] : 0;
+      int item = split ? work[0] : (int)blockIdx.x, tile = split ? work[1] : 0, drawn = 0;
+      int left = split ? work[2] : 0, index = split ? work[3] : 0;
       uint32_t n = 0, loads = 0;
       bool end = false;
       auto draw = [&]() {
         const int t = atomicAdd(P.ticket, 1);
         if (t == P.items - 1) *P.ticket = 0;  // every CTA draws until it is past the last item
         return (int)gridDim.x + t;
+      };
+      auto advance = [&](const Segment& a) {
+        left -= a.t1 - a.t0;
+        index += a.t1 - a.t0;
+        tile = 0;
+        if (split) {
+          ++item;
+        } else {
+          item = drawn;
+          if (item < P.items) drawn = draw();
+        }
       };
       if (!split) drawn = draw();
       int row = 0, bytes = 0;  // queries still to be copied: those of the segment published last
@@ -552,28 +606,21 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         while (!end) {
           end = item >= P.items || (split && left <= 0);
           if (end) break;
-          a.s = seen_rows(P, item);
+          a.item = split ? item : P.items - 1 - item;
+          a.s = seen_rows(P, a.item);
           a.tiles = tiles_of(a.s);
-          a.item = item;
           a.t0 = tile;
-          a.t1 = split ? (int)min((long long)a.tiles, tile + left) : a.tiles;
+          a.t1 = split ? min(a.tiles, tile + left) : a.tiles;
           a.index = index;
           more = a.t1 > tile;
-          left -= a.t1 - tile;
-          index += a.t1 - tile;
-          tile = 0;
-          if (split) {
-            ++item;
-          } else {
-            item = drawn;
-            if (item < P.items) drawn = draw();
-          }
-          if (more) break;  // else padding
+          if (more) break;
+          advance(a);  // padding
         }
         if (!more) a.t1 = 0;
         if (n >= kRing && !wait(&g_empty[n % kRing], n / kRing - 1)) break;
         ring[n % kRing] = a;
         mbar_arrive(&g_full[n % kRing]);
+        if (more) advance(a);
         const int next_row = more ? a.s.b * P.c.N * P.H + a.s.f0 : 0, next_bytes = more ? a.s.cols * D * 2 : 0;
         if (n == 0)
           row = next_row, bytes = next_bytes;  // the first segment's at once
@@ -595,11 +642,11 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         while (*abort_flag && item < P.items) item = drawn, drawn = item < P.items ? draw() : item;
       if (*abort_flag && loads > 0) mbar_wait_bounded(q_full, (loads - 1) & 1);
     }
-  } else if (R::kEpi && warp >= 4 && warp < 8) {
+  } else if (R::kEpi && warp >= 4 && warp < R::kMma) {
     uint32_t k = 0;
     while (next()) {
       k += g.t1 - g.t0;
-      if (!finish(warp & 3, 2, k - 1, (int)threadIdx.x - 128)) break;
+      if (!finish(k - 1, (int)threadIdx.x - 128)) break;
     }
   } else if (warp >= R::kRows) {
     // ---- rows: warp w of a group brings rows kTileRows * w .. of its group's tiles
@@ -609,6 +656,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     // of the swizzled rows once: rows r and r + 4 side by side for 16-byte units, eight rows for units
     // that expand to 64 bytes
     const int r8 = kFp4 ? lane & 7 : (lane >> 3) + 4 * ((lane >> 2) & 1), u0 = kFp4 ? lane >> 3 : lane & 3;
+    constexpr int kGroups = R::kTileRows / 8;
     uint32_t k = 0;
     int pending = -1;  // a stage whose copies were issued and not yet handed over
     bool ok = true;
@@ -618,7 +666,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
       if (v >= g.s.cnt) return -1;
       const int j = v < P.sinks ? v : v + g.s.jump;
       if (!P.c.paged) return g.s.b * P.c.kv_rows + j;
-      const int ps = P.c.cache.page_size, pg = (int)((uint32_t)j / (uint32_t)ps);
+      const int ps = P.c.cache.page_size, pg = P.by_page.of(j);
       const int page = __ldg(P.c.page_table + (long long)g.s.b * P.c.max_pages + pg);
       if (page >= 0 && page < P.c.cache.pages) return page * ps + (j - pg * ps);
       atomicOr(P.flag, 2);
@@ -629,21 +677,30 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
       __syncwarp();
       if (lane == 0) mbar_arrive(&c_full[st]);
     };
-    auto stage_free = [&](uint32_t st) {  // the whole warp's answer
-      const bool yes = k < nst || wait(&c_empty[st], k / nst - 1);
-      return __all_sync(0xffffffffu, yes) != 0;
+    auto flush = [&]() {
+      if (pending >= 0) {
+        cp_wait<0>();
+        hand_over(pending);
+        pending = -1;
+      }
     };
-    while (ok && next()) {
+    auto stage_free = [&](uint32_t st) {  // the whole warp's answer
+      if (!kFp4 && k >= nst && !__all_sync(0xffffffffu, mbar_test(&c_empty[st], ((k >> lst) - 1) & 1))) flush();
+      return __all_sync(0xffffffffu, k < nst || wait(&c_empty[st], (k >> lst) - 1)) != 0;
+    };
+    while (ok) {
+      if (!kFp4 && !__all_sync(0xffffffffu, mbar_test(&g_full[seg % kRing], (seg / kRing) & 1))) flush();
+      if (!next()) break;
 #pragma unroll 1
       for (int t = g.t0; t < g.t1; ++t, ++k) {
         if ((int)(k & 1) != grp) continue;
-        const uint32_t st = k % nst;
+        const uint32_t st = k & (nst - 1);
 #ifdef CSA_DEBUG_BOUNDS
-        if (P.test_stall && k == 0) break;  // test of the time-out path: a first tile never comes
+        if (P.test_stall && k == 0) break;  // test of the time-out path: the first tile never comes
 #endif
         const uint32_t dst = smem_addr(sC) + st * stage_bytes;
-        const int v0 = t * kTile + R::kTileRows * w + r8;
-        constexpr int kGroups = R::kTileRows / 8;
+        // lane l resolves rows l and l + 32 of the tile
+        const int e0 = entry(t * kTile + lane), e1 = entry(t * kTile + 32 + lane);
         if constexpr (kFp4) {
           // codes, expanded into the bf16 operand: a lane takes 32 codes and two scales (half a chunk) of
           // its row at a time; the next eight rows' are on their way while eight are expanded
@@ -651,12 +708,13 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
           uint4 code[4];
           uint32_t sc[4];
           auto load = [&](int i) {
-            const int row = entry(v0 + 8 * i);
-            const uint4* cp = reinterpret_cast<const uint4*>(P.c.cache.codes + (size_t)max(row, 0) * (D / 2)) + u0;
-            const uint16_t* sp = reinterpret_cast<const uint16_t*>(P.c.cache.scales + (size_t)max(row, 0) * (D / 16)) + u0;
+            const int r = R::kTileRows * w + 8 * i + r8, a = __shfl_sync(0xffffffffu, e0, r & 31),
+                      b = __shfl_sync(0xffffffffu, e1, r & 31), rr = r < 32 ? a : b;
+            const uint4* cp = reinterpret_cast<const uint4*>(P.c.cache.codes + (size_t)max(rr, 0) * (D / 2)) + u0;
+            const uint16_t* sp = reinterpret_cast<const uint16_t*>(P.c.cache.scales + (size_t)max(rr, 0) * (D / 16)) + u0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const bool live = row >= 0 && u0 + 4 * j < upr;
+              const bool live = rr >= 0 && u0 + 4 * j < upr;
               code[j] = live ? __ldg(cp + 4 * j) : make_uint4(0, 0, 0, 0);
               sc[j] = live ? __ldg(sp + 4 * j) : 0;
             }
@@ -692,43 +750,50 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
           }
           hand_over(st);
         } else {
-          int row[kGroups];
-#pragma unroll
-          for (int i = 0; i < kGroups; ++i) row[i] = entry(v0 + 8 * i);
-          if (pending >= 0 && k >= nst && !mbar_test(&c_empty[st], (k / nst - 1) & 1)) {
-            cp_wait<0>();
-            hand_over(pending);
-            pending = -1;
-          }
+          const int e = __shfl_sync(0xffffffffu, e0, 0);
+          const bool run = __all_sync(0xffffffffu, e0 >= 0 && e0 == e + lane && e1 == e + 32 + lane) != 0;
           if (!(ok = stage_free(st))) break;
-#pragma unroll
+          if (run) {
+            // 64 consecutive rows: one tensor copy
+            if (lane == 0) {
+              if (w == 0) {
+                mbar_arrive_expect_tx(&c_full[st], (uint32_t)stage_bytes);
+                tma_load_3d(sC + st * stage_bytes, &map_c, 0, e, 0, &c_full[st]);
+              } else {
+                mbar_arrive(&c_full[st]);
+              }
+            }
+            continue;
+          }
+#pragma unroll 1
           for (int i = 0; i < kGroups; ++i) {
-            const uint32_t r = R::kTileRows * w + 8 * i + r8, bytes = row[i] < 0 ? 0u : 16u;
-            const uint8_t* src = base + (size_t)max(row[i], 0) * (2 * D) + u0 * 16;
+            const int r = R::kTileRows * w + 8 * i + r8, ra = __shfl_sync(0xffffffffu, e0, r & 31),
+                      rb = __shfl_sync(0xffffffffu, e1, r & 31), rr = r < 32 ? ra : rb;
+            const uint32_t bytes = rr < 0 ? 0u : 16u;
+            const uint8_t* src = base + (size_t)max(rr, 0) * (2 * D) + u0 * 16;
             const uint32_t lo = dst + r * 128 + ((u0 ^ (r & 7)) << 4), hi = lo ^ 64;
-#pragma unroll 2
+#pragma unroll 4
             for (int c = 0; c < chunks; ++c) {
               cp_async16(lo + c * kChunkBytes, src + c * 128, bytes);
               cp_async16(hi + c * kChunkBytes, src + c * 128 + 64, bytes);
             }
           }
           cp_commit();
-          if (nst == 2) {
-            cp_wait<0>();
-            hand_over(st);
-          } else {
-            if (pending >= 0) {
-              cp_wait<1>();
-              hand_over(pending);
-            }
-            pending = st;
+          if (pending >= 0) {
+            cp_wait<1>();
+            hand_over(pending);
           }
+          pending = (int)st;
+          if (nst == 2) flush();
         }
       }
     }
     if constexpr (!kFp4) {
-      cp_wait<0>();
-      if (pending >= 0) hand_over(pending);
+      flush();
+      // after an abort: the tensor copies in flight land (a stage's last use)
+      if (*abort_flag && lane == 0 && w == 0)
+        for (uint32_t i = k > nst ? k - nst : 0; i < k; ++i)
+          if ((int)(i & 1) == grp) mbar_wait_bounded(&c_full[i & (nst - 1)], (i >> lst) & 1, 1000000);
     }
   } else if (warp == R::kMma) {
     // ---- MMAs: the whole warp runs the loop, one elected lane issues
@@ -748,14 +813,14 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         // their way when that one's weights are ready
         bool score = ns < n && ns <= nv + 1;
         if (score && ns > nv) {
-          const uint32_t st = (k + ns) % nst;
-          for (int spin = 0; score && !mbar_test(&c_full[st], ((k + ns) / nst) & 1); ++spin)
+          const uint32_t st = (k + ns) & (nst - 1);
+          for (int spin = 0; score && !mbar_test(&c_full[st], ((k + ns) >> lst) & 1); ++spin)
             score = spin < kSpins && !mbar_test(&p_full[(k + nv) & 1], ((k + nv) >> 1) & 1);
           score = __all_sync(0xffffffffu, score);
         }
-        const uint32_t kk = __shfl_sync(0xffffffffu, k + (score ? ns : nv), 0), st = kk % nst, buf = kk & 1;
+        const uint32_t kk = __shfl_sync(0xffffffffu, k + (score ? ns : nv), 0), st = kk & (nst - 1), buf = kk & 1;
         if (score) {
-          ok = wait(&c_full[st], kk / nst);
+          ok = wait(&c_full[st], kk >> lst);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after();
           const uint32_t d = tmem + oc + buf * kCols;
@@ -772,19 +837,24 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
           }
           ++ns;
         } else {
-          ok = wait(&p_full[buf], kk >> 1) && (nv > 0 || seg == 1 || wait(o_empty, seg - 2));
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (!(ok = __all_sync(0xffffffffu, wait(&p_full[buf], kk >> 1)))) break;
           tc_fence_after();
           uint64_t a = sw128_desc(c0 + st * stage_bytes, kChunkBytes);
           const uint64_t b = sw128_desc(p0 + buf * kPBytes, kChunkBytes);
 #pragma unroll 1
-          for (int x = 0; x < chunks; x += 2, a += 2 * kChunkBytes / 16)
+          for (int x = 0; x < chunks; x += 2, a += 2 * kChunkBytes / 16) {
+            if (nv == 0 && seg > 1) {  // the item before has been read out of this block
+              if (!(ok = __all_sync(0xffffffffu, wait(&o_empty[x >> 1], seg - 2)))) break;
+              tc_fence_after();
+            }
             if (leader) {
 #pragma unroll
               for (int y = 0; y < 4; ++y)
                 mma_bf16(tmem + (x >> 1) * kCols, a + 128 * y, b + 128 * y, x + 1 < chunks ? idesc_o : idesc_o64,
                          nv | y ? 1u : 0u);
             }
+          }
+          if (!ok) break;
           if (leader) {
             mma_commit(&c_empty[st]);
             mma_commit(&pv_done[buf]);
@@ -808,7 +878,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
       for (int i = 0; i < 16; ++i) l[i] = 0.0f;
       const bool several = g.s.tlo != g.s.thi;  // tokens: their rows differ
       if (several) {
-        if (threadIdx.x < kCols) colt[threadIdx.x] = min(g.s.thi, P.c.start + (g.s.f0 + (int)threadIdx.x) / P.H);
+        if (threadIdx.x < kCols) colt[threadIdx.x] = min(g.s.thi, P.c.start + P.by_heads.of(g.s.f0 + (int)threadIdx.x));
         group_sync(1);
       }
 #pragma unroll 1
@@ -823,21 +893,28 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(raw[i]);
         const int v0 = t * kTile, v1 = min(v0 + kTile, g.s.cnt), v = v0 + 16 * warp + (lane >> 2);
-        if (t == g.t0 && several) {  // the first row may be hidden from some tokens
+        if (t == g.t0) {
+          // the reference: the score of a row that every token of the item sees
+          const int vr = several && P.sinks == 0 && g.s.jump > 0 ? g.s.thi - g.s.tlo : 0;
+          const int jr = vr < P.sinks ? vr : vr + g.s.jump;
+          const bool seen = !several || (t == 0 && vr < min(kTile, g.s.cnt) && jr <= g.s.tlo &&
+                                         (!P.window || jr < P.sinks || jr > g.s.thi - P.window));
+          if (seen) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) m[i] = kFloor;
-        } else if (t == g.t0) {
-          if (warp == 0 && lane < 4) {
+            for (int h = 0; h < 2; ++h)
+              if (16 * warp + (lane >> 2) + 8 * h == vr) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float2*>(red + 8 * i + c2) =
-                  make_float2(fabsf(x[4 * i]) < INFINITY ? x[4 * i] * sl : kFloor,
-                              fabsf(x[4 * i + 1]) < INFINITY ? x[4 * i + 1] * sl : kFloor);
+                for (int i = 0; i < 8; ++i) {
+                  const float y0 = x[4 * i + 2 * h], y1 = x[4 * i + 2 * h + 1];
+                  *reinterpret_cast<float2*>(red + 8 * i + c2) =
+                      make_float2(fabsf(y0) < INFINITY ? y0 * sl : kFloor, fabsf(y1) < INFINITY ? y1 * sl : kFloor);
+                }
+              }
+            group_sync(1);
           }
-          group_sync(1);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 y = *reinterpret_cast<const float2*>(red + 8 * i + c2);
+            const float2 y = seen ? *reinterpret_cast<const float2*>(red + 8 * i + c2) : make_float2(kFloor, kFloor);
             m[2 * i] = y.x, m[2 * i + 1] = y.y;
           }
         }
@@ -896,7 +973,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
             spoilt |= __shfl_xor_sync(0xffffffffu, spoilt, 2);
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-              uint8_t* at = sC + (k % nst) * stage_bytes + (16 * warp + (lane >> 2) + 8 * h) * 128 + (lane & 3) * 32;
+              uint8_t* at = sC + (k & (nst - 1)) * stage_bytes + (16 * warp + (lane >> 2) + 8 * h) * 128 + (lane & 3) * 32;
               uint32_t bad = 0;
               if (spoilt >> h & 1)
 #pragma unroll 1
@@ -912,33 +989,36 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
                   *reinterpret_cast<uint32_t*>(at + (c >> 3) * kChunkBytes + (c & 7) * 4) = 0u;
             }
           }
-          float f[16];
+          // the queries' maxima over the tile, by way of the weights buffer (rows of 64): this thread's
+          // two rows, then a query a thread over the 32 pairs of rows
+          float* col = reinterpret_cast<float*>(sP + (k & 1) * kPBytes);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float2*>(col + (8 * warp + (lane >> 2)) * 64 + 8 * i + c2) =
+                make_float2(fmaxf(x[4 * i], x[4 * i + 2]), fmaxf(x[4 * i + 1], x[4 * i + 3]));
+          if (lane < 4 && warp == 0) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float y = fmaxf(x[4 * i + e], x[4 * i + 2 + e]);
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
-              f[2 * i + e] = y * sl;
-            }
-          if (lane < 4) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float2*>(red + warp * 64 + 8 * i + c2) = make_float2(f[2 * i], f[2 * i + 1]);
+            for (int i = 0; i < 8; ++i) *reinterpret_cast<float2*>(red + 8 * i + c2) = make_float2(m[2 * i], m[2 * i + 1]);
           }
           group_sync(1);
+          if (threadIdx.x < kCols) {
+            float y = kFloor;
+#pragma unroll 4
+            for (int i = 0; i < 32; ++i) y = fmaxf(y, col[i * 64 + threadIdx.x]);
+            // only the queries that need it: what a query gives does not depend on the others'
+            const float m0 = red[threadIdx.x], m1 = y * sl - m0 > kStep ? y * sl : m0;
+            red[threadIdx.x] = m1;
+            red[64 + threadIdx.x] = ex2(m0 - m1);
+          }
+          group_sync(1);
+          float f[16];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            float2 y = make_float2(m[2 * i], m[2 * i + 1]);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const float2 z = *reinterpret_cast<const float2*>(red + w * 64 + 8 * i + c2);
-              y.x = fmaxf(y.x, z.x), y.y = fmaxf(y.y, z.y);
-            }
-            f[2 * i] = ex2(m[2 * i] - y.x), f[2 * i + 1] = ex2(m[2 * i + 1] - y.y);
-            l[2 * i] *= f[2 * i], l[2 * i + 1] *= f[2 * i + 1];
+            const float2 y = *reinterpret_cast<const float2*>(red + 8 * i + c2),
+                         z = *reinterpret_cast<const float2*>(red + 64 + 8 * i + c2);
             m[2 * i] = y.x, m[2 * i + 1] = y.y;
+            f[2 * i] = z.x, f[2 * i + 1] = z.y;
+            l[2 * i] *= z.x, l[2 * i + 1] *= z.y;
           }
           if (t > g.t0) {
             ok = wait(&pv_done[(k & 1) ^ 1], (k - 1) >> 1);
@@ -984,11 +1064,9 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         if (lane == 0) mbar_arrive(&p_full[k & 1]);
       }
       if (!ok) break;
-      // the segment's end: sums over the warp's rows
+      // the segment's end: sums over rows, four lanes' of a warp left to the epilogue
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+      for (int i = 0; i < 16; ++i) l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
       if (R::kEpi && seg > 1) {
         ok = wait(l_empty, seg - 2);
         if (group_or(1, !ok)) {
@@ -996,19 +1074,20 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
           break;
         }
       }
-      if (lane < 4) {
+      if (lane < 16) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          *reinterpret_cast<float2*>(fin + warp * 64 + 8 * i + c2) = make_float2(l[2 * i], l[2 * i + 1]);
-          if (warp == 0) *reinterpret_cast<float2*>(fin + 256 + 8 * i + c2) = make_float2(m[2 * i], m[2 * i + 1]);
-        }
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float2*>(fin + (4 * warp + (lane >> 2)) * 64 + 8 * i + c2) = make_float2(l[2 * i], l[2 * i + 1]);
+      } else if (warp == 0 && lane < 20) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<float2*>(fin + 1024 + 8 * i + c2) = make_float2(m[2 * i], m[2 * i + 1]);
       }
       if constexpr (R::kEpi) {
         __syncwarp();
         if (lane == 0) mbar_arrive(l_full);
       } else {
         group_sync(1);
-        ok = finish(warp, 1, k - 1, (int)threadIdx.x);
+        ok = finish(k - 1, (int)threadIdx.x);
       }
     }
   }
@@ -1027,81 +1106,95 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
   if (warp == R::kMma) tmem_dealloc(tmem, tmem_cols);
 }
 
-// ---- pieces of split items joined: one CTA per record and 16 features (a warp's share of a fragment
-// load), a thread per four values of a piece.
+// ---- pieces of split items joined.
 //   M = max m_p;  out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p
-// The pieces are added in order by each of blockDim.y groups of threads and the groups' sums in order
-// after that: the result does not depend on timing.
-constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(1024) attention_join_kernel(const AttnParams P) {
-  extern __shared__ float wgt[];  // [pieces][64]
-  __shared__ float4 acc[4][kJoinThreads];
-  __shared__ __align__(16) uint16_t tile[kCols][16];
-  __shared__ float red[16][kCols], top[kCols], sum[kCols];
+// A thread takes four values (two queries, features d and d + 8) of every kGroups-th piece, kReps times
+// 16 features on; the groups' results are merged like pieces, in order: nothing depends on timing.
+// Few items have many pieces each (16 groups, the item over D / 4 CTAs), many items a few.
+template <int kLanes, int kGroups, int kReps>
+__global__ void __launch_bounds__(kLanes * kGroups) attention_join_kernel(const __grid_constant__ AttnParams P) {
+  __shared__ float4 acc[kGroups > 1 ? kGroups : 1][kLanes];
+  __shared__ float4 ml[kGroups > 1 ? kGroups : 1][kLanes];
+  __shared__ __align__(16) uint16_t tile[kLanes / 4][16];  // queries x 16 features
   griddep_wait();
   const int2 rec = P.record[blockIdx.x];
-  if (rec.x < 0) return;
-  const int n = rec.y, x = blockIdx.y >> 2, w = blockIdx.y & 3, i = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int grp = threadIdx.y, groups = blockDim.y, q = 8 * i + 2 * (lane & 3);
-  const Seen s = seen_rows(P, rec.x);
-  auto slot = [&](int p) { return 2 * ((int)blockIdx.x + p) + (p == 0 ? 1 : 0); };
-  {
-    // the pieces' weights: thread rows over pieces, a query a thread
-    const int tid = grp * kJoinThreads + threadIdx.x, qq = tid & 63, r0 = tid >> 6, nr = 4 * groups;
-    float t = kFloor, z = 0.0f;
-    for (int p = r0; p < n; p += nr) t = fmaxf(t, P.part_ml[slot(p) * kCols + qq].x);
-    red[r0][qq] = t;
-    __syncthreads();
-    for (int r = 0; r < nr; ++r) t = fmaxf(t, red[r][qq]);
-    __syncthreads();
-    for (int p = r0; p < n; p += nr) {
-      const float2 y = P.part_ml[slot(p) * kCols + qq];
-      const float f = ex2(y.x - t);
-      wgt[p * kCols + qq] = f;
-      z = fmaf(y.y, f, z);
-    }
-    red[r0][qq] = z;
-    __syncthreads();
-    if (r0 == 0) {
-      z = 0.0f;
-      for (int r = 0; r < nr; ++r) z += red[r][qq];
-      top[qq] = t, sum[qq] = z;
-    }
-    __syncthreads();
+  const Seen s = seen_rows(P, kGroups > 1 ? (int)blockIdx.x : max(rec.x, 0));
+  if (rec.x < 0 || s.cols == 0) return;
+  const int n = rec.y, cta = kGroups > 1 ? rec.x : (int)blockIdx.x, j0 = blockIdx.y * kLanes * kReps + threadIdx.x;  // of the piece's 16 D quads of values
+  const int lane = threadIdx.x & 31, grp = threadIdx.y, qt = 8 * (threadIdx.x >> 5) + 2 * (lane & 3);
+  const int q0 = 8 * ((j0 >> 5) & 7) - 8 * (int)(threadIdx.x >> 5), q = q0 + qt;  // the CTA's, the thread's first query
+  auto slot = [&](int p) { return 2 * (cta + p) + (p == 0 ? 1 : 0); };
+  auto stats = [&](int p) { return *reinterpret_cast<const float4*>(P.part_ml + slot(p) * kCols + q); };
+  float4 y = make_float4(kFloor, 0.0f, kFloor, 0.0f);  // maximum and sum of both queries
+#pragma unroll 4
+  for (int p = grp; p < n; p += kGroups) {
+    const float4 z = stats(p);
+    y.x = fmaxf(y.x, z.x), y.z = fmaxf(y.z, z.z);
   }
-  const float4* src = P.part + (x * 4 + w) * 256 + threadIdx.x;
-  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-  for (int p = grp; p < n; p += groups) {
-    const float4 o = src[(size_t)slot(p) * (kCols * P.D / 4)];
-    const float2 f = *reinterpret_cast<const float2*>(wgt + p * kCols + q);
-    a.x = fmaf(o.x, f.x, a.x), a.y = fmaf(o.y, f.y, a.y), a.z = fmaf(o.z, f.x, a.z), a.w = fmaf(o.w, f.y, a.w);
-  }
-  if (groups > 1) {
-    acc[grp][threadIdx.x] = a;
-    __syncthreads();
-    if (grp == 0)
-      for (int r = 1; r < groups; ++r) {
-        const float4 o = acc[r][threadIdx.x];
-        a.x += o.x, a.y += o.y, a.z += o.z, a.w += o.w;
+  float4 a[kReps];
+#pragma unroll
+  for (int r = 0; r < kReps; ++r) a[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+  for (int p = grp; p < n; p += kGroups) {
+    const float4 z = stats(p);
+    const float f0 = ex2(z.x - y.x), f1 = ex2(z.z - y.z);
+    y.y = fmaf(z.y, f0, y.y), y.w = fmaf(z.w, f1, y.w);
+    const float4* src = P.part + (size_t)slot(p) * (kCols * P.D / 4) + j0;
+#pragma unroll
+    for (int r = 0; r < kReps; ++r)
+      if (j0 + r * kLanes < 16 * P.D) {
+        const float4 o = src[r * kLanes];
+        a[r].x = fmaf(o.x, f0, a[r].x), a[r].y = fmaf(o.y, f1, a[r].y);
+        a[r].z = fmaf(o.z, f0, a[r].z), a[r].w = fmaf(o.w, f1, a[r].w);
       }
   }
-  const long long orow = (long long)s.b * P.c.N * P.H + s.f0, rows = (long long)P.c.B * P.c.N * P.H;
-  if (grp == 0) {
-    const float i0 = sum[q] == 0.0f ? 0.0f : 1.0f / sum[q], i1 = sum[q + 1] == 0.0f ? 0.0f : 1.0f / sum[q + 1];
-    tile[q][lane >> 2] = bf16_bits(a.x * i0), tile[q + 1][lane >> 2] = bf16_bits(a.y * i1);
-    tile[q][8 + (lane >> 2)] = bf16_bits(a.z * i0), tile[q + 1][8 + (lane >> 2)] = bf16_bits(a.w * i1);
-    if (P.c.lse && blockIdx.y == 0 && threadIdx.x < s.cols && in_bounds(orow + threadIdx.x, rows, P.flag)) {
-      const float z = sum[threadIdx.x];
-      P.c.lse[orow + threadIdx.x] = z == 0.0f ? -INFINITY : (top[threadIdx.x] + log2f(z)) * 0.693147180559945f;
+  if constexpr (kGroups > 1) {
+    acc[grp][threadIdx.x] = a[0], ml[grp][threadIdx.x] = y;
+    __syncthreads();
+    if (grp == 0) {
+      float2 top = make_float2(kFloor, kFloor);
+      for (int i = 0; i < kGroups; ++i)
+        top.x = fmaxf(top.x, ml[i][threadIdx.x].x), top.y = fmaxf(top.y, ml[i][threadIdx.x].z);
+      y = make_float4(top.x, 0.0f, top.y, 0.0f), a[0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int i = 0; i < kGroups; ++i) {
+        const float4 z = ml[i][threadIdx.x], o = acc[i][threadIdx.x];
+        const float f0 = ex2(z.x - top.x), f1 = ex2(z.z - top.y);
+        y.y = fmaf(z.y, f0, y.y), y.w = fmaf(z.w, f1, y.w);
+        a[0].x = fmaf(o.x, f0, a[0].x), a[0].y = fmaf(o.y, f1, a[0].y);
+        a[0].z = fmaf(o.z, f0, a[0].z), a[0].w = fmaf(o.w, f1, a[0].w);
+      }
     }
   }
-  __syncthreads();
-  // features 16 w of the last 64, else 32 w + 16 h of 128
-  const int d = (x | 1) < P.D / 64 ? (x >> 1) * 128 + 32 * w + 16 * (x & 1) : x * 64 + 16 * w;
-  const int r = threadIdx.x >> 1, u = threadIdx.x & 1;
-  if (grp == 0 && r < s.cols && r < kCols && in_bounds(orow + r, rows, P.flag))
-    *reinterpret_cast<uint4*>(P.c.out + (orow + r) * P.D + d + 8 * u) = *reinterpret_cast<const uint4*>(&tile[r][8 * u]);
+  const long long orow = (long long)s.b * P.c.N * P.H + s.f0, rows = (long long)P.c.B * P.c.N * P.H;
+  const float i0 = y.y == 0.0f ? 0.0f : 1.0f / y.y, i1 = y.w == 0.0f ? 0.0f : 1.0f / y.w;
+  if (grp == 0 && P.c.lse && j0 - threadIdx.x < 256 && lane < 4) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float t = e ? y.w : y.y;
+      if (q + e < s.cols && in_bounds(orow + q + e, rows, P.flag))
+        P.c.lse[orow + q + e] = t == 0.0f ? -INFINITY : ((e ? y.z : y.x) + log2f(t)) * 0.693147180559945f;
+    }
+  }
+#pragma unroll 1
+  for (int r = 0; r < kReps; ++r) {
+    const int at = (j0 + r * kLanes) >> 8, x = at >> 2, w = at & 3;  // the fragment load's half block and warp
+    if (x >= P.D / 64) break;
+    if (grp == 0) {
+      float4 v = a[0];
+#pragma unroll
+      for (int i = 1; i < kReps; ++i)
+        if (i == r) v = a[i];
+      tile[qt][lane >> 2] = bf16_bits(v.x * i0), tile[qt + 1][lane >> 2] = bf16_bits(v.y * i1);
+      tile[qt][8 + (lane >> 2)] = bf16_bits(v.z * i0), tile[qt + 1][8 + (lane >> 2)] = bf16_bits(v.w * i1);
+    }
+    __syncthreads();
+    // features 16 w of the last 64, else 32 w + 16 (x % 2) of 128
+    const int d = (x | 1) < P.D / 64 ? (x >> 1) * 128 + 32 * w + 16 * (x & 1) : x * 64 + 16 * w;
+    const int t = threadIdx.x >> 1, u = threadIdx.x & 1;
+    if (grp == 0 && t < kLanes / 4 && q0 + t < s.cols && in_bounds(orow + q0 + t, rows, P.flag))
+      *reinterpret_cast<uint4*>(P.c.out + (orow + q0 + t) * P.D + d + 8 * u) = *reinterpret_cast<const uint4*>(&tile[t][8 * u]);
+    __syncthreads();
+  }
 }
 
 // ---- host side
@@ -1113,7 +1206,7 @@ struct Shape {
 Shape attn_shape(int D, bool fp4) {
   Shape s;
   s.ctas = D <= 192 && !fp4 ? 2 : 1;
-  const int chunk = D / 64 * kChunkBytes, rest = 2 * kPBytes + 4 * kStageOut + kAuxBytes + 1024;
+  const int chunk = D / 64 * kChunkBytes, rest = 2 * kPBytes + 8 * kStageOut + kAuxBytes + 1024;
   const int budget = (s.ctas == 2 ? 113 : 227) * 1024 - rest;
   s.stages = 8;
   while (s.stages > 2 && (s.stages + 1) * chunk > budget) s.stages /= 2;
@@ -1141,7 +1234,6 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
     cudaError_t r = cudaFuncSetAttribute(attention_kernel<true, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (r == cudaSuccess) r = cudaFuncSetAttribute(attention_kernel<false, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (r == cudaSuccess) r = cudaFuncSetAttribute(attention_kernel<false, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (r == cudaSuccess) r = cudaFuncSetAttribute(attention_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
     return r;
   });
   if (e != cudaSuccess) return e;
@@ -1150,8 +1242,9 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
   P.c = call;
   P.H = a->heads;
   P.D = a->D;
-  P.window = a->window;
-  P.sinks = a->sinks;
+  // positions are below 2^30: a longer window is none, more sinks are all
+  P.window = a->window < (1 << 30) ? a->window : 0;
+  P.sinks = P.window == 0 ? 0 : a->sinks < (1 << 30) - 128 ? a->sinks : (1 << 30) - 128;
   P.per = (int)(((long long)call.N * a->heads + kCols - 1) / kCols);
   P.items = call.B * P.per;
   P.scale_log2 = (float)(a->scale * 1.4426950408889634);
@@ -1160,7 +1253,10 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
   P.part_ml = (float2*)((float*)a->workspace + (size_t)slots * kCols * a->D);
   P.record = (int2*)(P.part_ml + (size_t)slots * kCols);
   P.ticket = (int*)(P.record + slots);
-  P.stages = sh.stages;
+  while ((1 << P.log_stages) < sh.stages) ++P.log_stages;
+  P.by_per = Divisor(P.per);
+  P.by_heads = Divisor(P.H);
+  P.by_page = Divisor(call.paged ? call.cache.page_size : 1);
 #ifdef CSA_DEBUG_BOUNDS
   P.test_stall = getenv("CSA_TEST_STALL_LAST_STAGE") != nullptr;
   P.wait_ns = P.test_stall ? 200000000ull : kWaitNs;
@@ -1169,10 +1265,13 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
   long long most = call.paged ? (long long)call.max_pages * call.cache.page_size : (long long)call.start + call.N;
   const long long window = (long long)a->window + a->sinks + kCols / a->heads;
   if (a->window && most > window) most = window;
-  P.split = most > (long long)kJoinTiles * kTile;
+  // (a prompt with several items a CTA is not: drawing them, the longest first, balances as well)
+  P.split = most > (long long)kJoinTiles * kTile && (call.paged || P.items < 4 * most_ctas);
   const long long longest = most > kTile ? (most + kTile - 1) / kTile : 1, tiles = P.items * longest;
+  if (P.split && tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
   const long long shares = P.split ? tiles : P.items;
   const int grid = (int)(shares < most_ctas ? shares : most_ctas);
+  P.few = P.items * 8 <= grid;
   CUtensorMap mq;
   {
     cuuint64_t dims[2] = {(cuuint64_t)a->D, (cuuint64_t)call.B * call.N * a->heads};
@@ -1184,23 +1283,34 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  kernel<<<grid, threads, sh.smem, s>>>(mq, P);
+  CUtensorMap mc = mq;  // not used for codes
+  if (!fp4) {
+    // 64 consecutive rows, chunk by chunk of 64 features
+    cuuint64_t dims[3] = {64, call.paged ? (cuuint64_t)call.cache.pages * call.cache.page_size
+                                         : (cuuint64_t)call.B * call.kv_rows, (cuuint64_t)a->D / 64};
+    cuuint64_t strides[2] = {(cuuint64_t)a->D * 2, 128};
+    cuuint32_t box[3] = {64, kTile, (cuuint32_t)a->D / 64};
+    cuuint32_t es[3] = {1, 1, 1};
+    if (encode(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void*)(call.paged ? call.cache.latent : call.kv), dims, strides,
+               box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  kernel<<<grid, threads, sh.smem, s>>>(mq, mc, P);
   a->launches += 1;
   if ((e = cudaGetLastError()) != cudaSuccess || !P.split) return e;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, a->D / 16);
-  // few items have many pieces each: four groups of threads share them
-  cfg.blockDim = dim3(kJoinThreads, P.items * 8 <= grid ? 4 : 1);
-  // an item's pieces: every CTA has at least kMinTiles tiles
-  cfg.dynamicSmemBytes = kCols * sizeof(float) * (longest / kMinTiles + 2 < grid ? longest / kMinTiles + 2 : grid);
+  cfg.gridDim = P.few ? dim3(P.items, a->D / 4) : dim3(grid, (a->D + 127) / 128);
+  cfg.blockDim = P.few ? dim3(64, 16) : dim3(256, 1);
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   a->launches += 1;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel, P);
+  return P.few ? cudaLaunchKernelEx(&cfg, attention_join_kernel<64, 16, 1>, P)
+             : cudaLaunchKernelEx(&cfg, attention_join_kernel<256, 1, 8>, P);
 }
 
 }  // namespace csa

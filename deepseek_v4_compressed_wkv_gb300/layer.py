@@ -16,7 +16,6 @@ belong to that stream, and those passed in are kept for it.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -38,26 +37,37 @@ class _Cache(ctypes.Structure):
 def _want(name, t, dtype, shape, device):
     """The data pointer of a contiguous CUDA tensor of the given type and shape on the current
     device (a pointer into another GPU's memory would fault)."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
     if t.dtype != dtype:
         raise CSAError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise CSAError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_cuda or not t.is_contiguous():
         raise CSAError(f"{name} must be a contiguous CUDA tensor")
-    if t.get_device() != device:
-        raise CSAError(f"{name} is on {t.device}, but the current CUDA device is cuda:{device}")
-    return t.data_ptr()
+    raise CSAError(f"{name} is on {t.device}, but the current CUDA device is cuda:{device}")
 
 
-def _on(stream, *tensors):
-    """(stream handle, context for tensors made by the call): a stream that is not the current one
-    must own what the call makes and keep what it reads and writes until it is done with it."""
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream, contextlib.nullcontext()
-    for t in tensors:
-        if t is not None and t.is_cuda:
-            t.record_stream(stream)
-    return stream.cuda_stream, torch.cuda.stream(stream)
+# The current stream's handle of a device: the call behind torch.cuda.current_stream(), without the
+# object that it makes (3 of the 15 us that a small call takes on the host).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+class _Here:
+    """Tensors made by a call belong to its stream: a stream that is not the current one must own
+    what the call makes, and keep what it reads and writes until it is done with it."""
+    __slots__ = ("made",)
+
+    def __init__(self, stream, tensors):
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(stream)
+        self.made = torch.cuda.stream(stream)
+
+    def __call__(self, make, *args, **kw):
+        with self.made:
+            return make(*args, **kw)
 
 
 class PagedCache:
@@ -89,6 +99,7 @@ class PagedCache:
         self._ref = ctypes.addressof(self._struct)
         self._arrays = [t for t in (latent, codes, scales) if t is not None]
         self._flag = None
+        self._append = load_library().csa_cache_append
 
     @classmethod
     def allocate(cls, pages: int, page_size: int, head_dim: int, fp4: int = 0, device="cuda"):
@@ -124,11 +135,16 @@ class PagedCache:
         pt = _want("page_table", page_table, _I32, (B, page_table.shape[-1]), dev)
         fi = _want("first", first, _I32, (B,), dev)
         mk = None if mask is None else _want("mask", mask, _U8, (B,), dev)
-        s, _ = _on(stream, *self._arrays, *(entries.get(n) for n in ("latent", "codes", "scales")), page_table, first,
-                   mask, self._flag)
+        if stream is None:
+            s = _raw_stream(dev)
+        else:
+            _Here(stream, (*self._arrays, *(entries.get(n) for n in ("latent", "codes", "scales")), page_table, first, mask,
+                           self._flag))
+            s = stream.cuda_stream
         out = Out(*src, None)
-        _check(load_library().csa_cache_append(self._ref, ctypes.addressof(out), B, G, pt, page_table.shape[1], fi, mk,
-                                               self._flag.data_ptr(), s), "csa_cache_append")
+        rc = self._append(self._ref, ctypes.addressof(out), B, G, pt, page_table.shape[1], fi, mk, self._flag.data_ptr(), s)
+        if rc < 0:
+            _check(rc, "csa_cache_append")
 
     def status(self):
         """Raises CSAError if an append since the last call left an entry out (a negative index, an
@@ -184,14 +200,23 @@ class Attention:
         qp = _want("q", q, _BF16, shape, dev)
         kp = _want("kv", kv, _BF16, (B, kv.shape[1], self.head_dim), dev)
         lp = None if lens is None else _want("lens", lens, _I32, (B,), dev)
-        s, made = _on(stream, q, kv, lens, out, lse)
-        with made:
-            out = torch.empty(shape, dtype=_BF16, device=q.device) if out is None else out
-            lse = torch.empty(lshape, dtype=_F32, device=q.device) if lse is None else lse
-        _check(self._lib.csa_attention_prefill(self._h, qp, kp, B, N, start_pos, kv.shape[1], lp,
-                                               _want("out", out, _BF16, shape, dev), _want("lse", lse, _F32, lshape, dev),
-                                               s), "csa_attention_prefill")
+        op, out, zp, lse, s = self._outputs(q, out, lse, shape, lshape, dev, stream, (q, kv, lens, out, lse))
+        rc = self._lib.csa_attention_prefill(self._h, qp, kp, B, N, start_pos, kv.shape[1], lp, op, zp, s)
+        if rc < 0:
+            _check(rc, "csa_attention_prefill")
         return out, lse
+
+    def _outputs(self, q, out, lse, shape, lshape, dev, stream, used):
+        """(pointer, out, pointer, lse, stream handle) of a call."""
+        if stream is None:
+            out = torch.empty_like(q) if out is None else out
+            lse = torch.empty(lshape, dtype=_F32, device=q.device) if lse is None else lse
+            s = _raw_stream(dev)
+        else:
+            make, s = _Here(stream, used), stream.cuda_stream
+            out = make(torch.empty_like, q) if out is None else out
+            lse = make(torch.empty, lshape, dtype=_F32, device=q.device) if lse is None else lse
+        return _want("out", out, _BF16, shape, dev), out, _want("lse", lse, _F32, lshape, dev), lse, s
 
     def decode(self, q, cache: PagedCache, page_table, lens, out=None, lse=None, stream=None):
         """q bf16 [B, heads, head_dim]: one new token a sequence, at position lens[b] - 1 (lens int32
@@ -208,21 +233,23 @@ class Attention:
         width = page_table.shape[1]
         pp = _want("page_table", page_table, _I32, (B, width), dev)
         lp = _want("lens", lens, _I32, (B,), dev)
-        s, made = _on(stream, q, page_table, lens, out, lse, *cache._arrays)
-        with made:
-            out = torch.empty(shape, dtype=_BF16, device=q.device) if out is None else out
-            lse = torch.empty(lshape, dtype=_F32, device=q.device) if lse is None else lse
-        _check(self._lib.csa_attention_decode(self._h, qp, cache._ref, pp, width, lp, B,
-                                              _want("out", out, _BF16, shape, dev), _want("lse", lse, _F32, lshape, dev),
-                                              s), "csa_attention_decode")
+        op, out, zp, lse, s = self._outputs(q, out, lse, shape, lshape, dev, stream,
+                                            (q, page_table, lens, out, lse, *cache._arrays))
+        rc = self._lib.csa_attention_decode(self._h, qp, cache._ref, pp, width, lp, B, op, zp, s)
+        if rc < 0:
+            _check(rc, "csa_attention_decode")
         return out, lse
 
     def kernel_launches(self) -> int:
         return _check(self._lib.csa_attention_launches(self._h), "csa_attention_launches")
 
     def device_status(self, stream=None):
-        s, _ = _on(stream)
+        s = _raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
         return _check(self._lib.csa_attention_status(self._h, s), "csa_attention_status")
+
+
+def _call(make, *args, **kw):
+    return make(*args, **kw)
 
 
 def rmsnorm_residual_q8(x, residual, gain, eps: float = 1e-6, scale_block: int = 128, y: bool = True, inplace: bool = False,
@@ -242,16 +269,18 @@ def rmsnorm_residual_q8(x, residual, gain, eps: float = 1e-6, scale_block: int =
     xp = _want("x", x, _BF16, x.shape, dev)
     rp = None if residual is None else _want("residual", residual, _BF16, x.shape, dev)
     gp = _want("gain", gain, _F32, (dim,), dev)
-    s, made = _on(stream, x, residual, gain)
-    lead = x.shape[:-1]
-    with made:
-        total = x if residual is None else residual if inplace else torch.empty_like(x)
-        yt = torch.empty_like(x) if y else None
-        q = torch.empty(x.shape, dtype=_E4M3, device=x.device)
-        scales = torch.empty((*lead, dim // (scale_block or dim)), dtype=_E8M0 if scale_block == 32 else _F32,
-                             device=x.device)
-    _check(load_library().csa_rmsnorm_residual_q8(xp, rp, gp, x.numel() // dim, dim, eps, scale_block,
-                                                  None if residual is None else total.data_ptr(),
-                                                  None if yt is None else yt.data_ptr(), q.data_ptr(), scales.data_ptr(),
-                                                  s), "csa_rmsnorm_residual_q8")
+    if stream is None:
+        make, s = _call, _raw_stream(dev)
+    else:
+        make, s = _Here(stream, (x, residual, gain)), stream.cuda_stream
+    total = x if residual is None else residual if inplace else make(torch.empty_like, x)
+    yt = make(torch.empty_like, x) if y else None
+    q = make(torch.empty_like, x, dtype=_E4M3)
+    scales = make(torch.empty, (*x.shape[:-1], dim // (scale_block or dim)), dtype=_E8M0 if scale_block == 32 else _F32,
+                  device=x.device)
+    rc = load_library().csa_rmsnorm_residual_q8(xp, rp, gp, x.numel() // dim, dim, eps, scale_block,
+                                                None if residual is None else total.data_ptr(),
+                                                None if yt is None else yt.data_ptr(), q.data_ptr(), scales.data_ptr(), s)
+    if rc < 0:
+        _check(rc, "csa_rmsnorm_residual_q8")
     return {"residual": total, "y": yt, "q": q, "scales": scales}
