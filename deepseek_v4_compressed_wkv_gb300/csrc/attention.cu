@@ -14,9 +14,9 @@
 // and O^T takes D / 128 * 64 columns of tensor memory (256 of 512 at D = 512) where queries as rows
 // would take all of it.  The scores come back with a row per TMEM lane in the matrix-fragment shape.
 // The reference need not be the maximum: bf16 weights and f32 sums keep their relative precision as
-// long as it is near.  It begins as the first row's score, and is only renewed (as the maximum so
-// far, with O^T and l scaled) when a score passes it by 2^16; taking the maximum over rows costs
-// shuffles and an exchange between the warps that most tiles need not pay.
+// long as it is near.  It begins as 0, and is only renewed (as the tile's maximum, with O^T and l
+// scaled) when a score passes it by 16 base-2 steps, or when a query's first scores are all below
+// -64: taking the maximum over rows costs an exchange between the warps that most tiles need not pay.
 //
 // What bounds it (probes on GB300, cycles): a 64 x 64 x 16 MMA takes 32 and a 128 x 64 x 16 one 48
 // (shared-memory reads of both operands at 128 bytes a cycle), so a tile of 64 rows at D = 512 costs
@@ -49,9 +49,10 @@ constexpr int kStageOut = 1024;                // a warp's staging of 16 queries
 constexpr int kJoinTiles = 6;   // items longer than this are split
 constexpr int kMinTiles = 4;    // a split call gives a CTA at least this many tiles
 constexpr float kStep = 16.0f;  // base-2 steps a score may pass the reference by
-constexpr float kFloor = -1e38f;  // a reference that any score passes
+constexpr float kLow = -64.0f;  // where the first scores are all lower, 0 is no reference for them
+constexpr float kFloor = -1e38f;  // the maximum of no scores
 constexpr int kSpins = 1 << 16;   // polls of two barriers before the MMA warp waits for one of them
-constexpr int kAuxBytes = 6144;   // barriers, flags, references and sums
+constexpr int kAuxBytes = 6400;   // barriers, flags, references and sums
 
 // Division of 31-bit numbers by a number known to the host: with l = ceil(log2 d) and
 // m = floor(2^(31 + l) / d) + 1, n / d = (m n) >> (31 + l) (Granlund and Montgomery, 1994).
@@ -156,17 +157,6 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) 
       : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
-      : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
 // The same over 32 columns, not waiting.
 __device__ __forceinline__ void tmem_ld_half(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -175,6 +165,15 @@ __device__ __forceinline__ void tmem_ld_half(uint32_t taddr, uint32_t (&r)[16]) 
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_half(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 template <bool kTrans>
@@ -214,19 +213,18 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t wait_ns) {
   return mbar_wait(bar, parity, abort_flag, wait_ns);
 }
-// A barrier of some warps (1: softmax, 2: epilogue); group_or gives every thread whether any passed
+// A barrier of eight warps (1: softmax, 2: epilogue); group_or gives every thread whether any passed
 // true.
-template <int kThreads = 128>
+constexpr int kWorkers = 8, kGroupThreads = 256;
 __device__ __forceinline__ void group_sync(int id) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kGroupThreads) : "memory");
 }
-template <int kThreads = 128>
 __device__ __forceinline__ bool group_or(int id, bool p) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)p), "r"(id), "n"(kThreads)
+      : "r"((uint32_t)p), "r"(id), "n"(kGroupThreads)
       : "memory");
   return r != 0;
 }
@@ -266,16 +264,15 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t scale2) {
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// ---- the kernel's warps: 0-3 softmax (TMEM lane quarter = warp); with one CTA an SM 4-11 the
-// epilogue, which reads O^T while the softmax warps go on with the next item (up to D = 192 two CTAs
-// share an SM instead, whose softmax warps read their own O^T); then one that issues the MMAs, one
-// for the queries' copies, and the rows' warps in two groups that take alternate tiles (one group's
-// tile can be in flight while the other waits for its stage).
+// ---- the kernel's warps: 0-7 softmax (TMEM lane quarter = warp % 4, 32 of the 64 queries each); with
+// one CTA an SM 8-15 the epilogue, which reads O^T while the softmax warps go on with the next item (up
+// to D = 192 two CTAs share an SM instead, whose softmax warps read their own O^T); then one that
+// issues the MMAs, one that schedules and copies the queries, and the rows' warps in two groups that
+// take alternate tiles (one group's tile can be in flight while the other waits for its stage).
 template <bool kFp4, int kCtas>
 struct Roles {
   static constexpr bool kEpi = kCtas == 1;
-  static constexpr int kEpiWarps = kEpi ? 8 : 4;  // warps that read O^T
-  static constexpr int kMma = kEpi ? 4 + kEpiWarps : 4, kQ = kMma + 1, kRows = kMma + 2;
+  static constexpr int kMma = kEpi ? 16 : 8, kQ = kMma + 1, kRows = kMma + 2;
   static constexpr int kRowWarps = kCtas == 2 ? 2 : 4;
   static constexpr int kGroupWarps = kRowWarps / 2;
   static constexpr int kTileRows = kTile / kGroupWarps;  // rows of a tile a warp brings
@@ -314,11 +311,11 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   Segment* ring = (Segment*)(aux + 384);
   int* work = (int*)(aux + 640);  // split calls: first item, tile, tiles, tile index, end, tiles of a share, shares with one more
-  float* red = (float*)(aux + 704);   // [2][64] references, factors; the scan's sums before
-  float* fin = red + 128;             // [16][64] sums over rows, [64] references
+  float* red = (float*)(aux + 704);   // [3][64] references, factors, first maxima; the scan's sums before
+  float* fin = red + 192;             // [16][64] sums over rows, [64] references
   float* inv = fin + 1088;            // [64] 1 / sum
   int* colt = (int*)(inv + 64);       // [64] the queries' positions
-  static_assert(704 + (128 + 1088 + 64 + 64) * 4 <= kAuxBytes, "aux region");
+  static_assert(704 + (192 + 1088 + 64 + 64) * 4 <= kAuxBytes, "aux region");
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 #ifdef CSA_DEBUG_BOUNDS
@@ -337,7 +334,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], kWorkers);
       mbar_init(&pv_done[i], 1);
     }
     for (int i = 0; i < kRing; ++i) {
@@ -346,9 +343,9 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&o_empty[i], R::kEpiWarps);
-    mbar_init(l_full, 4);
-    mbar_init(l_empty, R::kEpiWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(&o_empty[i], kWorkers);
+    mbar_init(l_full, kWorkers);
+    mbar_init(l_empty, kWorkers);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -445,16 +442,16 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     return g.t1 > 0;
   };
 
-  // ---- an item's end, by the warps that read O^T's lane quarters (warp % 4; two warps of a quarter
+  // ---- an item's end, by eight warps, two of each of O^T's lane quarters (warp % 4: they
   // share its columns or halves): the sums over rows in `fin`, O^T (complete with tile kl) scaled to
   // out, or left as a piece.  A block of 128 features is given back to the MMAs as soon as it has
   // been read.  False after an abort.
   auto finish = [&](uint32_t kl, int tid) -> bool {
-    constexpr int bar = R::kEpi ? 2 : 1, kEpiThreads = 32 * R::kEpiWarps, kTwo = R::kEpiWarps / 4;
+    constexpr int bar = R::kEpi ? 2 : 1;
     const int w = warp & 3, half = tid >> 7;
     bool ok = !R::kEpi || wait(l_full, seg - 1);
     ok = ok && wait(&pv_done[kl & 1], kl >> 1);
-    if (group_or<kEpiThreads>(bar, !ok)) return false;
+    if (group_or(bar, !ok)) return false;
     tc_fence_after();
     const bool whole = g.t0 == 0 && g.t1 == g.tiles;
     // a piece: slot 0 of the CTA for its first segment's, 1 for its last's (an item's first piece)
@@ -473,10 +470,10 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         if (P.c.lse && tid < g.s.cols && in_bounds(orow + tid, rows, P.flag))
           P.c.lse[orow + tid] = l == 0.0f ? -INFINITY : (m + lg) * 0.693147180559945f;
       } else {
-        P.part_ml[slot * kCols + tid] = make_float2(m, l);
+        P.part_ml[slot * kCols + tid] = make_float2(l == 0.0f ? kFloor : m, l);  // (no row: no reference either)
       }
     }
-    group_sync<kEpiThreads>(bar);
+    group_sync(bar);
     if (R::kEpi && lane == 0) mbar_arrive(l_empty);
     auto give_back = [&](int block) {
       tc_fence_before();
@@ -493,7 +490,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
       tmem_ld_half(base + 32 * half, o[0]);
       tmem_ld_half(base + 32 * half + (16u << 16), o[1]);
 #pragma unroll 1
-      for (int step = half; step < steps; step += kTwo) {
+      for (int step = half; step < steps; step += 2) {
         const int x = step & ~1, c = step & 1;
         const bool full = x + 1 < chunks;
         float2 f[4];
@@ -511,15 +508,15 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
               v[i][h][j] = bf16x2(__uint_as_float(o[h][4 * q + 2 * (j & 1)]) * f[q].x,
                                   __uint_as_float(o[h][4 * q + 2 * (j & 1) + 1]) * f[q].y);
             }
-        if (kTwo == 2 || c == 1) give_back(step >> 1);
-        if (step + kTwo < steps) {
-          const uint32_t at = base + 32 * (step + kTwo);  // 64 columns a block of 128 features
+        give_back(step >> 1);
+        if (step + 2 < steps) {
+          const uint32_t at = base + 32 * (step + 2);  // 64 columns a block of 128 features
           tmem_ld_half(at, o[0]);
           tmem_ld_half(at + (16u << 16), o[1]);
         }
         // to [query][32 features] by transposed stores, 16 queries at a time; 16-byte units swizzled
         // against conflicts
-        uint8_t* stage = sO + (warp - (R::kEpi ? 4 : 0)) * kStageOut;
+        uint8_t* stage = sO + (warp & 7) * kStageOut;
         const int r = 8 * (lane >> 4) + (lane & 7), u = lane & 3;
         uint16_t* dst = P.c.out + (orow + 32 * c + (lane >> 2)) * D + x * 64 + w * (full ? 32 : 16) + 8 * u;
 #pragma unroll
@@ -547,7 +544,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     } else {
       float4* dst = P.part + (size_t)slot * (kCols * D / 4) + w * 256 + lane;
 #pragma unroll 1
-      for (int x = half; x < ((chunks + 1) & ~1); x += kTwo) {  // half x % 2 of 16 lanes a warp of a block
+      for (int x = half; x < ((chunks + 1) & ~1); x += 2) {  // half x % 2 of 16 lanes a warp of a block
         if (x < chunks) {
         uint32_t o[32];
         tmem_ld_frag(base + (x >> 1) * kCols + ((uint32_t)(16 * (x & 1)) << 16), o);
@@ -556,7 +553,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
           dst[(x * 32 + i) * 32] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         }
-        if (kTwo == 2 || (x & 1)) give_back(x >> 1);
+        give_back(x >> 1);
       }
       if (g.t0 == 0 && tid == 0) {
         // the item ends in the CTA whose share holds its last tile
@@ -622,11 +619,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         mbar_arrive(&g_full[n % kRing]);
         if (more) advance(a);
         const int next_row = more ? a.s.b * P.c.N * P.H + a.s.f0 : 0, next_bytes = more ? a.s.cols * D * 2 : 0;
-        if (n == 0)
-          row = next_row, bytes = next_bytes;  // the first segment's at once
-        else if (more)
-          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(P.c.q + (size_t)next_row * D), "r"(next_bytes)
-                       : "memory");
+        if (n == 0) row = next_row, bytes = next_bytes;  // the first segment's at once
         if (bytes > 0) {
           if (loads > 0 && !wait(q_empty, loads - 1)) break;
           mbar_arrive_expect_tx(q_full, chunks * kChunkBytes);
@@ -642,11 +635,11 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         while (*abort_flag && item < P.items) item = drawn, drawn = item < P.items ? draw() : item;
       if (*abort_flag && loads > 0) mbar_wait_bounded(q_full, (loads - 1) & 1);
     }
-  } else if (R::kEpi && warp >= 4 && warp < R::kMma) {
+  } else if (R::kEpi && warp >= 8 && warp < 16) {
     uint32_t k = 0;
     while (next()) {
       k += g.t1 - g.t0;
-      if (!finish(k - 1, (int)threadIdx.x - 128)) break;
+      if (!finish(k - 1, (int)threadIdx.x - 256)) break;
     }
   } else if (warp >= R::kRows) {
     // ---- rows: warp w of a group brings rows kTileRows * w .. of its group's tiles
@@ -691,6 +684,11 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     while (ok) {
       if (!kFp4 && !__all_sync(0xffffffffu, mbar_test(&g_full[seg % kRing], (seg / kRing) & 1))) flush();
       if (!next()) break;
+      // these warps are ahead of the others: they ask the segment's queries into L2 (as plain prefetches:
+      // a bulk one holds up the tensor copies behind it)
+      const uint8_t* qrow = (const uint8_t*)(P.c.q + ((size_t)g.s.b * P.c.N * P.H + g.s.f0) * D);
+      for (int x = 128 * ((int)threadIdx.x - 32 * R::kRows); x < g.s.cols * D * 2; x += 128 * 32 * R::kRowWarps)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(qrow + x));
 #pragma unroll 1
       for (int t = g.t0; t < g.t1; ++t, ++k) {
         if ((int)(k & 1) != grp) continue;
@@ -802,80 +800,89 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
                    idesc_o64 = idesc_bf16(64, kCols) | kTransposed;
     const uint32_t c0 = smem_addr(sC), p0 = smem_addr(sP);
     const uint64_t qd = sw128_desc(smem_addr(sQ), 16);
-    uint32_t k = 0;  // tiles of earlier segments
-    bool ok = true;
-    while (ok && next()) {
-      ok = __all_sync(0xffffffffu, wait(q_full, seg - 1));
-      const uint32_t n = g.t1 - g.t0;
-      uint32_t ns = 0, nv = 0;  // tiles whose scores, whose values have been issued
-      while (ok && nv < n) {
-        // a tile's scores go ahead of the values of the one before it, unless its rows are still on
-        // their way when that one's weights are ready
-        bool score = ns < n && ns <= nv + 1;
-        if (score && ns > nv) {
-          const uint32_t st = (k + ns) & (nst - 1);
-          for (int spin = 0; score && !mbar_test(&c_full[st], ((k + ns) >> lst) & 1); ++spin)
-            score = spin < kSpins && !mbar_test(&p_full[(k + nv) & 1], ((k + nv) >> 1) & 1);
-          score = __all_sync(0xffffffffu, score);
-        }
-        const uint32_t kk = __shfl_sync(0xffffffffu, k + (score ? ns : nv), 0), st = kk & (nst - 1), buf = kk & 1;
-        if (score) {
-          ok = wait(&c_full[st], kk >> lst);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          tc_fence_after();
-          const uint32_t d = tmem + oc + buf * kCols;
-          uint64_t a = sw128_desc(c0 + st * stage_bytes, 16), b = qd;  // addresses in units of 16 bytes
-#pragma unroll 1
-          for (int x = 0; x < chunks; ++x, a += kChunkBytes / 16, b += kChunkBytes / 16)
-            if (leader) {
-#pragma unroll
-              for (int y = 0; y < 4; ++y) mma_bf16(d, a + 2 * y, b + 2 * y, idesc_s, x | y ? 1u : 0u);
-            }
-          if (leader) {
-            mma_commit(&s_full[buf]);
-            if (ns + 1 == n) mma_commit(q_empty);
-          }
-          ++ns;
-        } else {
-          if (!(ok = __all_sync(0xffffffffu, wait(&p_full[buf], kk >> 1)))) break;
-          tc_fence_after();
-          uint64_t a = sw128_desc(c0 + st * stage_bytes, kChunkBytes);
-          const uint64_t b = sw128_desc(p0 + buf * kPBytes, kChunkBytes);
-#pragma unroll 1
-          for (int x = 0; x < chunks; x += 2, a += 2 * kChunkBytes / 16) {
-            if (nv == 0 && seg > 1) {  // the item before has been read out of this block
-              if (!(ok = __all_sync(0xffffffffu, wait(&o_empty[x >> 1], seg - 2)))) break;
-              tc_fence_after();
-            }
-            if (leader) {
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                mma_bf16(tmem + (x >> 1) * kCols, a + 128 * y, b + 128 * y, x + 1 < chunks ? idesc_o : idesc_o64,
-                         nv | y ? 1u : 0u);
-            }
-          }
-          if (!ok) break;
-          if (leader) {
-            mma_commit(&c_empty[st]);
-            mma_commit(&pv_done[buf]);
-          }
-          ++nv;
-        }
-        __syncwarp();
+    // Tiles in order; the scores of tile ks go ahead of the values of tile kv, at most two before them, also
+    // into the next segment, unless their rows or queries are still on their way when tile kv's weights
+    // are ready.
+    uint32_t ks = 0, kv = 0, ts = 0, ns = 0;       // the next tiles; tile ts of the ns of ks's segment
+    uint32_t first = 0, seg_of[2] = {0, 0};        // per parity: a segment's first tile, its segment
+    bool ok = true, end = false;
+    int spin = 0;
+    auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity & 1)) != 0; };
+    while (ok) {
+      if (!end && ts == ns && ks - kv < 2 && (ks == kv || ready(&g_full[seg % kRing], seg / kRing))) {
+        end = !next();
+        ts = 0, ns = end ? 0 : g.t1 - g.t0;
       }
-      k += n;
+      if (ks == kv && ts == ns) break;
+      bool score = ts < ns && ks - kv < 2;
+      if (score && ks > kv) {
+        score = (ts > 0 || ready(q_full, seg - 1)) && ready(&c_full[ks & (nst - 1)], ks >> lst);
+        if (!score && spin < kSpins && !ready(&p_full[kv & 1], kv >> 1)) {
+          ++spin;
+          continue;
+        }
+      }
+      spin = 0;
+      const uint32_t kk = __shfl_sync(0xffffffffu, score ? ks : kv, 0), st = kk & (nst - 1), buf = kk & 1;
+      if (score) {
+        ok = (ts > 0 || wait(q_full, seg - 1)) && wait(&c_full[st], kk >> lst);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + oc + buf * kCols;
+        uint64_t a = sw128_desc(c0 + st * stage_bytes, 16), b = qd;  // addresses in units of 16 bytes
+#pragma unroll 1
+        for (int x = 0; x < chunks; ++x, a += kChunkBytes / 16, b += kChunkBytes / 16)
+          if (leader) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mma_bf16(d, a + 2 * y, b + 2 * y, idesc_s, x | y ? 1u : 0u);
+          }
+        if (leader) {
+          mma_commit(&s_full[buf]);
+          if (ts + 1 == ns) mma_commit(q_empty);
+        }
+        first = ts == 0 ? first | (1u << buf) : first & ~(1u << buf);
+        seg_of[0] = buf ? seg_of[0] : seg, seg_of[1] = buf ? seg : seg_of[1];
+        ++ks, ++ts;
+      } else {
+        if (!(ok = __all_sync(0xffffffffu, wait(&p_full[buf], kk >> 1)))) break;
+        tc_fence_after();
+        const bool begin = first >> buf & 1;
+        const uint32_t vseg = buf ? seg_of[1] : seg_of[0];
+        uint64_t a = sw128_desc(c0 + st * stage_bytes, kChunkBytes);
+        const uint64_t b = sw128_desc(p0 + buf * kPBytes, kChunkBytes);
+#pragma unroll 1
+        for (int x = 0; x < chunks; x += 2, a += 2 * kChunkBytes / 16) {
+          if (begin && vseg > 1) {  // the item before has been read out of this block
+            if (!(ok = __all_sync(0xffffffffu, wait(&o_empty[x >> 1], vseg - 2)))) break;
+            tc_fence_after();
+          }
+          if (leader) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              mma_bf16(tmem + (x >> 1) * kCols, a + 128 * y, b + 128 * y, x + 1 < chunks ? idesc_o : idesc_o64,
+                       !begin || y ? 1u : 0u);
+          }
+        }
+        if (!ok) break;
+        if (leader) {
+          mma_commit(&c_empty[st]);
+          mma_commit(&pv_done[buf]);
+        }
+        ++kv;
+      }
+      __syncwarp();
     }
   } else {
-    // ---- softmax
-    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    const int c2 = 2 * (lane & 3);
+    // ---- softmax: a warp has 16 rows (its lane quarter's) of 32 queries (half `hq`)
+    const int qt = warp & 3, hq = warp >> 2, c2 = 32 * hq + 2 * (lane & 3);  // columns c2 + 8 i + e
+    const uint32_t lanes = (uint32_t)(32 * qt) << 16;
     const float sl = P.scale_log2;
     uint32_t k = 0;
     bool ok = true;
     while (ok && next()) {
-      float m[16], l[16];
+      float m[8], l[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) l[i] = 0.0f;
+      for (int i = 0; i < 8; ++i) m[i] = l[i] = 0.0f;
       const bool several = g.s.tlo != g.s.thi;  // tokens: their rows differ
       if (several) {
         if (threadIdx.x < kCols) colt[threadIdx.x] = min(g.s.thi, P.c.start + P.by_heads.of(g.s.f0 + (int)threadIdx.x));
@@ -887,50 +894,26 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         // the weights buffer is free once the tile two before has been used
         if (ok && k >= 2) ok = wait(&pv_done[k & 1], (k >> 1) - 1);
         tc_fence_after();
-        uint32_t raw[32];
-        tmem_ld_frag(tmem + oc + (k & 1) * kCols + lanes, raw);
-        float x[32];
+        uint32_t raw[16];
+        tmem_ld_half(tmem + oc + (k & 1) * kCols + 32 * hq + lanes, raw);
+        tmem_ld_wait();
+        float x[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(raw[i]);
-        const int v0 = t * kTile, v1 = min(v0 + kTile, g.s.cnt), v = v0 + 16 * warp + (lane >> 2);
-        if (t == g.t0) {
-          // the reference: the score of a row that every token of the item sees
-          const int vr = several && P.sinks == 0 && g.s.jump > 0 ? g.s.thi - g.s.tlo : 0;
-          const int jr = vr < P.sinks ? vr : vr + g.s.jump;
-          const bool seen = !several || (t == 0 && vr < min(kTile, g.s.cnt) && jr <= g.s.tlo &&
-                                         (!P.window || jr < P.sinks || jr > g.s.thi - P.window));
-          if (seen) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (16 * warp + (lane >> 2) + 8 * h == vr) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float y0 = x[4 * i + 2 * h], y1 = x[4 * i + 2 * h + 1];
-                  *reinterpret_cast<float2*>(red + 8 * i + c2) =
-                      make_float2(fabsf(y0) < INFINITY ? y0 * sl : kFloor, fabsf(y1) < INFINITY ? y1 * sl : kFloor);
-                }
-              }
-            group_sync(1);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 y = seen ? *reinterpret_cast<const float2*>(red + 8 * i + c2) : make_float2(kFloor, kFloor);
-            m[2 * i] = y.x, m[2 * i + 1] = y.y;
-          }
-        }
-        bool renew = !ok;
+        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(raw[i]);
+        const int v0 = t * kTile, v1 = min(v0 + kTile, g.s.cnt), v = v0 + 16 * qt + (lane >> 2);
+        bool renew = !ok || (several && t < g.t0 + 2);  // (every token's first row is in the first two tiles)
         uint32_t spoilt = 0;  // bits 0, 1: this thread's rows hold a NaN or infinity that a token must not see
         if (several) {
           // rows that only some of the item's tokens see
-          const int first = max(v0, P.sinks);
+          const int begin = max(v0, P.sinks);
           if ((v1 - 1 < P.sinks ? v1 - 1 : v1 - 1 + g.s.jump) > g.s.tlo ||
-              (P.window && first < v1 && first + g.s.jump <= g.s.thi - P.window)) {
+              (P.window && begin < v1 && begin + g.s.jump <= g.s.thi - P.window)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int vv = v + 8 * h, j = vv < P.sinks ? vv : vv + g.s.jump;
               const int low = P.window && vv >= P.sinks ? j + P.window : 0x7fffffff;  // hidden from there on
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
+              for (int i = 0; i < 4; ++i) {
                 const int2 tc = *reinterpret_cast<const int2*>(colt + 8 * i + c2);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -952,16 +935,29 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         }
         if (v0 + kTile > g.s.cnt) {  // rows past the last one
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i) {
             if (v >= g.s.cnt) x[4 * i] = x[4 * i + 1] = -INFINITY;
             if (v + 8 >= g.s.cnt) x[4 * i + 2] = x[4 * i + 3] = -INFINITY;
           }
         }
+        // the largest step past a reference; on a first tile the largest score that is there and too low
+        float past = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            renew = renew || fmaf(fmaxf(x[4 * i + e], x[4 * i + 2 + e]), sl, -m[2 * i + e]) > kStep;
+          for (int e = 0; e < 2; ++e) past = fmaxf(past, fmaf(fmaxf(x[4 * i + e], x[4 * i + 2 + e]), sl, -m[2 * i + e]));
+        renew = renew || past > kStep;
+        if (t == g.t0) {
+          float low = INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float y = fmaxf(x[4 * i + e], x[4 * i + 2 + e]) * sl;
+              low = fminf(low, y > -INFINITY ? y : 0.0f);
+            }
+          renew = renew || low < kLow;
+        }
         if (group_or(1, renew)) {
           if (group_or(1, !ok)) {
             ok = false;
@@ -973,32 +969,33 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
             spoilt |= __shfl_xor_sync(0xffffffffu, spoilt, 2);
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-              uint8_t* at = sC + (k & (nst - 1)) * stage_bytes + (16 * warp + (lane >> 2) + 8 * h) * 128 + (lane & 3) * 32;
+              uint8_t* at = sC + (k & (nst - 1)) * stage_bytes + (16 * qt + (lane >> 2) + 8 * h) * 128 + (lane & 3) * 32;
               uint32_t bad = 0;
               if (spoilt >> h & 1)
 #pragma unroll 1
                 for (int c = 0; c < 8 * chunks; ++c) {
-                  const uint32_t y = *reinterpret_cast<const uint32_t*>(at + (c >> 3) * kChunkBytes + (c & 7) * 4);
+                  const uint32_t y = *reinterpret_cast<const volatile uint32_t*>(at + (c >> 3) * kChunkBytes + (c & 7) * 4);
                   bad |= (y & 0x7F80u) == 0x7F80u || (y & 0x7F800000u) == 0x7F800000u;
                 }
               bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
               bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+              group_sync(1);  // (the other half's warp may look at the same row)
               if (bad)
 #pragma unroll 1
                 for (int c = 0; c < 8 * chunks; ++c)
-                  *reinterpret_cast<uint32_t*>(at + (c >> 3) * kChunkBytes + (c & 7) * 4) = 0u;
+                  *reinterpret_cast<volatile uint32_t*>(at + (c >> 3) * kChunkBytes + (c & 7) * 4) = 0u;
             }
           }
           // the queries' maxima over the tile, by way of the weights buffer (rows of 64): this thread's
           // two rows, then a query a thread over the 32 pairs of rows
           float* col = reinterpret_cast<float*>(sP + (k & 1) * kPBytes);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float2*>(col + (8 * warp + (lane >> 2)) * 64 + 8 * i + c2) =
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float2*>(col + (8 * qt + (lane >> 2)) * 64 + 8 * i + c2) =
                 make_float2(fmaxf(x[4 * i], x[4 * i + 2]), fmaxf(x[4 * i + 1], x[4 * i + 3]));
-          if (lane < 4 && warp == 0) {
+          if (lane < 4 && qt == 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) *reinterpret_cast<float2*>(red + 8 * i + c2) = make_float2(m[2 * i], m[2 * i + 1]);
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(red + 8 * i + c2) = make_float2(m[2 * i], m[2 * i + 1]);
           }
           group_sync(1);
           if (threadIdx.x < kCols) {
@@ -1006,18 +1003,18 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
 #pragma unroll 4
             for (int i = 0; i < 32; ++i) y = fmaxf(y, col[i * 64 + threadIdx.x]);
             // only the queries that need it: what a query gives does not depend on the others'
-            const float m0 = red[threadIdx.x], m1 = y * sl - m0 > kStep ? y * sl : m0;
+            const bool before = t > g.t0 && (!several || red[128 + threadIdx.x] > kFloor);  // it has seen a row
+            const float m0 = red[threadIdx.x], m1 = y * sl - m0 > kStep || (!before && y > kFloor && y * sl < kLow) ? y * sl : m0;
+            if (several) red[128 + threadIdx.x] = before ? 0.0f : y;
             red[threadIdx.x] = m1;
-            red[64 + threadIdx.x] = ex2(m0 - m1);
+            red[64 + threadIdx.x] = before ? ex2(m0 - m1) : 1.0f;
           }
           group_sync(1);
-          float f[16];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i) {
             const float2 y = *reinterpret_cast<const float2*>(red + 8 * i + c2),
                          z = *reinterpret_cast<const float2*>(red + 64 + 8 * i + c2);
             m[2 * i] = y.x, m[2 * i + 1] = y.y;
-            f[2 * i] = z.x, f[2 * i + 1] = z.y;
             l[2 * i] *= z.x, l[2 * i + 1] *= z.y;
           }
           if (t > g.t0) {
@@ -1029,23 +1026,29 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
             tc_fence_after();
 #pragma unroll 1
             for (int x2 = 0; x2 < chunks; ++x2) {  // half x2 % 2 of the block of 128 features
-              const uint32_t at = tmem + (x2 >> 1) * kCols + lanes + ((uint32_t)(16 * (x2 & 1)) << 16);
-              uint32_t o[32];
-              tmem_ld_frag(at, o);
+              const uint32_t at = tmem + (x2 >> 1) * kCols + 32 * hq + lanes + ((uint32_t)(16 * (x2 & 1)) << 16);
+              uint32_t o[16];
+              tmem_ld_half(at, o);
+              tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                o[i] = __float_as_uint(__uint_as_float(o[i]) * f[2 * (i >> 2) + (i & 1)]);
-              tmem_st_frag(at, o);
+              for (int i = 0; i < 4; ++i) {
+                const float2 z = *reinterpret_cast<const float2*>(red + 64 + 8 * i + c2);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  o[4 * i + 2 * h] = __float_as_uint(__uint_as_float(o[4 * i + 2 * h]) * z.x);
+                  o[4 * i + 2 * h + 1] = __float_as_uint(__uint_as_float(o[4 * i + 2 * h + 1]) * z.y);
+                }
+              }
+              tmem_st_half(at, o);
             }
-          } else {
-            group_sync(1);  // `red` has been read
           }
+          group_sync(1);  // `red` has been read
         }
         // weights [row][64 queries] as 128-byte swizzled rows; matrices of a store: rows 0-7 and 8-15 of
         // two groups of 8 queries
-        const uint32_t at = smem_addr(sP) + (k & 1) * kPBytes + (16 * warp + (lane & 15)) * 128;
+        const uint32_t at = smem_addr(sP) + (k & 1) * kPBytes + (16 * qt + (lane & 15)) * 128;
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
+        for (int i = 0; i < 4; i += 2) {
           uint32_t pk[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -1056,7 +1059,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
             l[2 * q + 1] += p1;
             pk[j] = bf16x2(p0, p1);
           }
-          stmatrix4<false>(at + (((i + (lane >> 4)) ^ (lane & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+          stmatrix4<false>(at + (((4 * hq + i + (lane >> 4)) ^ (lane & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
         }
         fence_async_shared();
         tc_fence_before();
@@ -1066,7 +1069,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
       if (!ok) break;
       // the segment's end: sums over rows, four lanes' of a warp left to the epilogue
 #pragma unroll
-      for (int i = 0; i < 16; ++i) l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
+      for (int i = 0; i < 8; ++i) l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
       if (R::kEpi && seg > 1) {
         ok = wait(l_empty, seg - 2);
         if (group_or(1, !ok)) {
@@ -1076,11 +1079,11 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
       }
       if (lane < 16) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float2*>(fin + (4 * warp + (lane >> 2)) * 64 + 8 * i + c2) = make_float2(l[2 * i], l[2 * i + 1]);
-      } else if (warp == 0 && lane < 20) {
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float2*>(fin + (4 * qt + (lane >> 2)) * 64 + 8 * i + c2) = make_float2(l[2 * i], l[2 * i + 1]);
+      } else if (qt == 0 && lane < 20) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) *reinterpret_cast<float2*>(fin + 1024 + 8 * i + c2) = make_float2(m[2 * i], m[2 * i + 1]);
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(fin + 1024 + 8 * i + c2) = make_float2(m[2 * i], m[2 * i + 1]);
       }
       if constexpr (R::kEpi) {
         __syncwarp();
