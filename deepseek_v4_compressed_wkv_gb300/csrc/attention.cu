@@ -51,7 +51,6 @@ constexpr int kMinTiles = 4;    // a split call gives a CTA at least this many t
 constexpr float kStep = 16.0f;  // base-2 steps a score may pass the reference by
 constexpr float kLow = -64.0f;  // where the first scores are all lower, 0 is no reference for them
 constexpr float kFloor = -1e38f;  // the maximum of no scores
-constexpr int kSpins = 1 << 16;   // polls of two barriers before the MMA warp waits for one of them
 constexpr int kAuxBytes = 6400;   // barriers, flags, references and sums
 
 // Division of 31-bit numbers by a number known to the host: with l = ceil(log2 d) and
@@ -266,13 +265,15 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t scale2) {
 
 // ---- the kernel's warps: 0-7 softmax (TMEM lane quarter = warp % 4, 32 of the 64 queries each); with
 // one CTA an SM 8-15 the epilogue, which reads O^T while the softmax warps go on with the next item (up
-// to D = 192 two CTAs share an SM instead, whose softmax warps read their own O^T); then one that
-// issues the MMAs, one that schedules and copies the queries, and the rows' warps in two groups that
-// take alternate tiles (one group's tile can be in flight while the other waits for its stage).
+// to D = 192 two CTAs share an SM instead, whose softmax warps read their own O^T); then two that
+// issue the MMAs (scores run up to two tiles ahead of values, also into the next item, without one
+// loop having to look out for both), one that schedules and copies the queries, and the rows' warps in
+// two groups that take alternate tiles (one group's tile can be in flight while the other waits for
+// its stage).
 template <bool kFp4, int kCtas>
 struct Roles {
   static constexpr bool kEpi = kCtas == 1;
-  static constexpr int kMma = kEpi ? 16 : 8, kQ = kMma + 1, kRows = kMma + 2;
+  static constexpr int kMma = kEpi ? 16 : 8, kVal = kMma + 1, kQ = kMma + 2, kRows = kMma + 3;
   static constexpr int kRowWarps = kCtas == 2 ? 2 : 4;
   static constexpr int kGroupWarps = kRowWarps / 2;
   static constexpr int kTileRows = kTile / kGroupWarps;  // rows of a tile a warp brings
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     for (int i = 0; i < 4; ++i) mbar_init(&o_empty[i], kWorkers);
     mbar_init(l_full, kWorkers);
     mbar_init(l_empty, kWorkers);
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, 2);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     prefetch_map(&map_q);
@@ -794,38 +795,19 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
           if ((int)(i & 1) == grp) mbar_wait_bounded(&c_full[i & (nst - 1)], (i >> lst) & 1, 1000000);
     }
   } else if (warp == R::kMma) {
-    // ---- MMAs: the whole warp runs the loop, one elected lane issues
+    // ---- scores: the whole warp runs the loop, one elected lane issues
     const bool leader = elect_one();
-    const uint32_t idesc_s = idesc_bf16(64, kCols), idesc_o = idesc_bf16(128, kCols) | kTransposed,
-                   idesc_o64 = idesc_bf16(64, kCols) | kTransposed;
-    const uint32_t c0 = smem_addr(sC), p0 = smem_addr(sP);
+    const uint32_t idesc = idesc_bf16(64, kCols), c0 = smem_addr(sC);
     const uint64_t qd = sw128_desc(smem_addr(sQ), 16);
-    // Tiles in order; the scores of tile ks go ahead of the values of tile kv, at most two before them, also
-    // into the next segment, unless their rows or queries are still on their way when tile kv's weights
-    // are ready.
-    uint32_t ks = 0, kv = 0, ts = 0, ns = 0;       // the next tiles; tile ts of the ns of ks's segment
-    uint32_t first = 0, seg_of[2] = {0, 0};        // per parity: a segment's first tile, its segment
-    bool ok = true, end = false;
-    int spin = 0;
-    auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity & 1)) != 0; };
-    while (ok) {
-      if (!end && ts == ns && ks - kv < 2 && (ks == kv || ready(&g_full[seg % kRing], seg / kRing))) {
-        end = !next();
-        ts = 0, ns = end ? 0 : g.t1 - g.t0;
-      }
-      if (ks == kv && ts == ns) break;
-      bool score = ts < ns && ks - kv < 2;
-      if (score && ks > kv) {
-        score = (ts > 0 || ready(q_full, seg - 1)) && ready(&c_full[ks & (nst - 1)], ks >> lst);
-        if (!score && spin < kSpins && !ready(&p_full[kv & 1], kv >> 1)) {
-          ++spin;
-          continue;
-        }
-      }
-      spin = 0;
-      const uint32_t kk = __shfl_sync(0xffffffffu, score ? ks : kv, 0), st = kk & (nst - 1), buf = kk & 1;
-      if (score) {
-        ok = (ts > 0 || wait(q_full, seg - 1)) && wait(&c_full[st], kk >> lst);
+    uint32_t k = 0;
+    bool ok = true;
+    while (ok && next()) {
+      ok = __all_sync(0xffffffffu, wait(q_full, seg - 1));
+#pragma unroll 1
+      for (int t = g.t0; ok && t < g.t1; ++t, ++k) {
+        const uint32_t kk = __shfl_sync(0xffffffffu, k, 0), st = kk & (nst - 1), buf = kk & 1;
+        // the buffer's scores of two tiles before have been read, and the rows have landed
+        ok = (k < 2 || wait(&p_full[buf], (kk >> 1) - 1)) && wait(&c_full[st], kk >> lst);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         const uint32_t d = tmem + oc + buf * kCols;
@@ -834,32 +816,41 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         for (int x = 0; x < chunks; ++x, a += kChunkBytes / 16, b += kChunkBytes / 16)
           if (leader) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) mma_bf16(d, a + 2 * y, b + 2 * y, idesc_s, x | y ? 1u : 0u);
+            for (int y = 0; y < 4; ++y) mma_bf16(d, a + 2 * y, b + 2 * y, idesc, x | y ? 1u : 0u);
           }
         if (leader) {
           mma_commit(&s_full[buf]);
-          if (ts + 1 == ns) mma_commit(q_empty);
+          if (t + 1 == g.t1) mma_commit(q_empty);
         }
-        first = ts == 0 ? first | (1u << buf) : first & ~(1u << buf);
-        seg_of[0] = buf ? seg_of[0] : seg, seg_of[1] = buf ? seg : seg_of[1];
-        ++ks, ++ts;
-      } else {
+        __syncwarp();
+      }
+    }
+  } else if (warp == R::kVal) {
+    // ---- values, likewise
+    const bool leader = elect_one();
+    const uint32_t idesc = idesc_bf16(128, kCols) | kTransposed, idesc64 = idesc_bf16(64, kCols) | kTransposed;
+    const uint32_t c0 = smem_addr(sC), p0 = smem_addr(sP);
+    uint32_t k = 0;
+    bool ok = true;
+    while (ok && next()) {
+#pragma unroll 1
+      for (int t = g.t0; ok && t < g.t1; ++t, ++k) {
+        const uint32_t kk = __shfl_sync(0xffffffffu, k, 0), st = kk & (nst - 1), buf = kk & 1;
         if (!(ok = __all_sync(0xffffffffu, wait(&p_full[buf], kk >> 1)))) break;
         tc_fence_after();
-        const bool begin = first >> buf & 1;
-        const uint32_t vseg = buf ? seg_of[1] : seg_of[0];
+        const bool begin = __shfl_sync(0xffffffffu, (int)(t == g.t0), 0);
         uint64_t a = sw128_desc(c0 + st * stage_bytes, kChunkBytes);
         const uint64_t b = sw128_desc(p0 + buf * kPBytes, kChunkBytes);
 #pragma unroll 1
         for (int x = 0; x < chunks; x += 2, a += 2 * kChunkBytes / 16) {
-          if (begin && vseg > 1) {  // the item before has been read out of this block
-            if (!(ok = __all_sync(0xffffffffu, wait(&o_empty[x >> 1], vseg - 2)))) break;
+          if (begin && seg > 1) {  // the item before has been read out of this block
+            if (!(ok = __all_sync(0xffffffffu, wait(&o_empty[x >> 1], seg - 2)))) break;
             tc_fence_after();
           }
           if (leader) {
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              mma_bf16(tmem + (x >> 1) * kCols, a + 128 * y, b + 128 * y, x + 1 < chunks ? idesc_o : idesc_o64,
+              mma_bf16(tmem + (x >> 1) * kCols, a + 128 * y, b + 128 * y, x + 1 < chunks ? idesc : idesc64,
                        !begin || y ? 1u : 0u);
           }
         }
@@ -868,9 +859,8 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
           mma_commit(&c_empty[st]);
           mma_commit(&pv_done[buf]);
         }
-        ++kv;
+        __syncwarp();
       }
-      __syncwarp();
     }
   } else {
     // ---- softmax: a warp has 16 rows (its lane quarter's) of 32 queries (half `hq`)
@@ -1099,7 +1089,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
   __syncthreads();
   if (*abort_flag) {
     if (threadIdx.x == 0) atomicOr(P.flag, 4);
-    if (warp == R::kMma && elect_one()) {  // the lane that issued them
+    if ((warp == R::kMma || warp == R::kVal) && elect_one()) {  // the lanes that issued them
       mma_commit(mma_done);
       mbar_wait_bounded(mma_done, 0);
     }
