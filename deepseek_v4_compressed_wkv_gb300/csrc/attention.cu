@@ -51,7 +51,7 @@ constexpr int kMinTiles = 4;    // a split call gives a CTA at least this many t
 constexpr float kStep = 16.0f;  // base-2 steps a score may pass the reference by
 constexpr float kLow = -64.0f;  // where the first scores are all lower, 0 is no reference for them
 constexpr float kFloor = -1e38f;  // the maximum of no scores
-constexpr int kAuxBytes = 6400;   // barriers, flags, references and sums
+constexpr int kAuxBytes = 6144;   // barriers, flags, references and sums
 
 // Division of 31-bit numbers by a number known to the host: with l = ceil(log2 d) and
 // m = floor(2^(31 + l) / d) + 1, n / d = (m n) >> (31 + l) (Granlund and Montgomery, 1994).
@@ -263,28 +263,22 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t scale2) {
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// ---- the kernel's warps: 0-7 softmax (TMEM lane quarter = warp % 4, 32 of the 64 queries each); with
-// one CTA an SM 8-15 the epilogue, which reads O^T while the softmax warps go on with the next item (up
-// to D = 192 two CTAs share an SM instead, whose softmax warps read their own O^T); then two that
-// issue the MMAs (scores run up to two tiles ahead of values, also into the next item, without one
-// loop having to look out for both), one that schedules and copies the queries, and the rows' warps in
-// two groups that take alternate tiles (one group's tile can be in flight while the other waits for
-// its stage).
-template <bool kFp4, int kCtas>
-struct Roles {
-  static constexpr bool kEpi = kCtas == 1;
-  static constexpr int kMma = kEpi ? 16 : 8, kVal = kMma + 1, kQ = kMma + 2, kRows = kMma + 3;
-  static constexpr int kRowWarps = kCtas == 2 ? 2 : 4;
-  static constexpr int kGroupWarps = kRowWarps / 2;
-  static constexpr int kTileRows = kTile / kGroupWarps;  // rows of a tile a warp brings
-  static constexpr int kThreads = 32 * (kRows + kRowWarps);
-};
+// ---- the kernel's warps: 0-7 softmax (TMEM lane quarter = warp % 4, 32 of the 64 queries each); 8-15 the
+// epilogue, which reads O^T while the softmax warps go on with the next item; then two that issue the
+// MMAs (scores run up to two tiles ahead of values, also into the next item, without one loop having to
+// look out for both), one that schedules and copies the queries, and the rows' warps in two groups that
+// take alternate tiles (one group's tile can be in flight while the other waits for its stage).
+// One CTA an SM at every D: two of half the warps shared an SM up to D = 192 (their softmax warps
+// reading their own O^T) and took 118 us where this takes 66 (2 x 1777 tokens, D 128, window 512).
+constexpr int kEpiWarp = 8, kMmaWarp = 16, kValWarp = 17, kQWarp = 18, kRowWarp = 19;
+constexpr int kRowWarps = 4, kRowGroup = kRowWarps / 2;  // two warps bring a tile
+constexpr int kTileRows = kTile / kRowGroup;             // 32 rows each
+constexpr int kAttnThreads = 32 * (kRowWarp + kRowWarps);
 
-template <bool kFp4, int kCtas>
-__global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
+template <bool kFp4>
+__global__ void __launch_bounds__(kAttnThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_c,
                      const __grid_constant__ AttnParams P) {
-  using R = Roles<kFp4, kCtas>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const int D = P.D, chunks = D / 64;
@@ -312,11 +306,11 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   Segment* ring = (Segment*)(aux + 384);
   int* work = (int*)(aux + 640);  // split calls: first item, tile, tiles, tile index, end, tiles of a share, shares with one more
-  float* red = (float*)(aux + 704);   // [3][64] references, factors, first maxima; the scan's sums before
-  float* fin = red + 192;             // [16][64] sums over rows, [64] references
+  float* red = (float*)(aux + 704);   // [2][64] references, factors; the scan's sums before
+  float* fin = red + 128;             // [16][64] sums over rows, [64] references
   float* inv = fin + 1088;            // [64] 1 / sum
   int* colt = (int*)(inv + 64);       // [64] the queries' positions
-  static_assert(704 + (192 + 1088 + 64 + 64) * 4 <= kAuxBytes, "aux region");
+  static_assert(704 + (128 + 1088 + 64 + 64) * 4 <= kAuxBytes, "aux region");
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 #ifdef CSA_DEBUG_BOUNDS
@@ -330,7 +324,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 8; ++s) {
-      mbar_init(&c_full[s], R::kGroupWarps);
+      mbar_init(&c_full[s], kRowGroup);
       mbar_init(&c_empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -340,7 +334,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&g_full[i], 1);
-      mbar_init(&g_empty[i], R::kThreads / 32 - 1);
+      mbar_init(&g_empty[i], kAttnThreads / 32 - 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -354,12 +348,12 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
   }
   const uint32_t oc = (uint32_t)((D + 127) / 128) * kCols;  // columns of O^T; two score buffers follow
   const uint32_t tmem_cols = oc + 2 * kCols <= 256 ? 256 : 512;
-  if (warp == R::kMma) tmem_alloc(tmem_slot, tmem_cols);
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, tmem_cols);
   griddep_launch_dependents();
 
   if (blockIdx.x == 0 && P.c.lens) {  // lengths out of range are taken as the nearest end
     const int most = P.c.paged ? P.c.max_pages * P.c.cache.page_size : P.c.N;
-    for (int b = threadIdx.x; b < P.c.B; b += R::kThreads) {
+    for (int b = threadIdx.x; b < P.c.B; b += kAttnThreads) {
       const int n = P.c.lens[b];
       if (n < 0 || n > most) atomicOr(P.flag, 1);
     }
@@ -367,7 +361,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
   if (P.split) {
     // ---- the CTA's share of the call's tiles: every CTA adds up the items' tiles (threads over
     // contiguous items) and finds its own first one
-    const int per = (P.items + R::kThreads - 1) / R::kThreads, lo = min(P.items, per * (int)threadIdx.x),
+    const int per = (P.items + kAttnThreads - 1) / kAttnThreads, lo = min(P.items, per * (int)threadIdx.x),
               hi = min(P.items, lo + per);
     int sum = 0, top = 0, all = 0;  // (the host has made sure that the call's tiles fit)
 #pragma unroll 1
@@ -386,8 +380,8 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     if (lane == 31) ws[warp] = pre, ws[32 + warp] = top;
     __syncthreads();
     {
-      const int y = lane < R::kThreads / 32 ? ws[lane] : 0;
-      top = lane < R::kThreads / 32 ? ws[32 + lane] : 0;
+      const int y = lane < kAttnThreads / 32 ? ws[lane] : 0;
+      top = lane < kAttnThreads / 32 ? ws[32 + lane] : 0;
       pre += __reduce_add_sync(0xffffffffu, lane < warp ? y : 0) - sum;  // tiles before this thread's items
       sum = pre + sum;                                                   // and with them
       top = __reduce_max_sync(0xffffffffu, top);
@@ -448,11 +442,10 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
   // out, or left as a piece.  A block of 128 features is given back to the MMAs as soon as it has
   // been read.  False after an abort.
   auto finish = [&](uint32_t kl, int tid) -> bool {
-    constexpr int bar = R::kEpi ? 2 : 1;
     const int w = warp & 3, half = tid >> 7;
-    bool ok = !R::kEpi || wait(l_full, seg - 1);
+    bool ok = wait(l_full, seg - 1);
     ok = ok && wait(&pv_done[kl & 1], kl >> 1);
-    if (group_or(bar, !ok)) return false;
+    if (group_or(2, !ok)) return false;
     tc_fence_after();
     const bool whole = g.t0 == 0 && g.t1 == g.tiles;
     // a piece: slot 0 of the CTA for its first segment's, 1 for its last's (an item's first piece)
@@ -474,8 +467,8 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         P.part_ml[slot * kCols + tid] = make_float2(l == 0.0f ? kFloor : m, l);  // (no row: no reference either)
       }
     }
-    group_sync(bar);
-    if (R::kEpi && lane == 0) mbar_arrive(l_empty);
+    group_sync(2);
+    if (lane == 0) mbar_arrive(l_empty);
     auto give_back = [&](int block) {
       tc_fence_before();
       __syncwarp();
@@ -567,7 +560,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
     return true;
   };
 
-  if (warp == R::kQ) {
+  if (warp == kQWarp) {
     // ---- scheduling and queries (one lane).  A split call's segments are the CTA's share; otherwise
     // items are drawn one at a time from the last (a prompt's longest) on, the CTA's first by its own
     // number: SMs differ in speed, items in length and padding in place.  The CTA that draws the last
@@ -636,21 +629,21 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         while (*abort_flag && item < P.items) item = drawn, drawn = item < P.items ? draw() : item;
       if (*abort_flag && loads > 0) mbar_wait_bounded(q_full, (loads - 1) & 1);
     }
-  } else if (R::kEpi && warp >= 8 && warp < 16) {
+  } else if (warp >= kEpiWarp && warp < kEpiWarp + kWorkers) {
     uint32_t k = 0;
     while (next()) {
       k += g.t1 - g.t0;
       if (!finish(k - 1, (int)threadIdx.x - 256)) break;
     }
-  } else if (warp >= R::kRows) {
+  } else if (warp >= kRowWarp) {
     // ---- rows: warp w of a group brings rows kTileRows * w .. of its group's tiles
-    const int grp = (warp - R::kRows) / R::kGroupWarps, w = (warp - R::kRows) % R::kGroupWarps;
+    const int grp = (warp - kRowWarp) / kRowGroup, w = (warp - kRowWarp) % kRowGroup;
     const uint8_t* base = (const uint8_t*)(P.c.paged ? P.c.cache.latent : P.c.kv);
     // eight rows at a time, four lanes a row, such that the eight lanes of a quarter warp hit every bank
     // of the swizzled rows once: rows r and r + 4 side by side for 16-byte units, eight rows for units
     // that expand to 64 bytes
     const int r8 = kFp4 ? lane & 7 : (lane >> 3) + 4 * ((lane >> 2) & 1), u0 = kFp4 ? lane >> 3 : lane & 3;
-    constexpr int kGroups = R::kTileRows / 8;
+    constexpr int kGroups = kTileRows / 8;
     uint32_t k = 0;
     int pending = -1;  // a stage whose copies were issued and not yet handed over
     bool ok = true;
@@ -688,7 +681,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
       // these warps are ahead of the others: they ask the segment's queries into L2 (as plain prefetches:
       // a bulk one holds up the tensor copies behind it)
       const uint8_t* qrow = (const uint8_t*)(P.c.q + ((size_t)g.s.b * P.c.N * P.H + g.s.f0) * D);
-      for (int x = 128 * ((int)threadIdx.x - 32 * R::kRows); x < g.s.cols * D * 2; x += 128 * 32 * R::kRowWarps)
+      for (int x = 128 * ((int)threadIdx.x - 32 * kRowWarp); x < g.s.cols * D * 2; x += 128 * 32 * kRowWarps)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(qrow + x));
 #pragma unroll 1
       for (int t = g.t0; t < g.t1; ++t, ++k) {
@@ -707,7 +700,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
           uint4 code[4];
           uint32_t sc[4];
           auto load = [&](int i) {
-            const int r = R::kTileRows * w + 8 * i + r8, a = __shfl_sync(0xffffffffu, e0, r & 31),
+            const int r = kTileRows * w + 8 * i + r8, a = __shfl_sync(0xffffffffu, e0, r & 31),
                       b = __shfl_sync(0xffffffffu, e1, r & 31), rr = r < 32 ? a : b;
             const uint4* cp = reinterpret_cast<const uint4*>(P.c.cache.codes + (size_t)max(rr, 0) * (D / 2)) + u0;
             const uint16_t* sp = reinterpret_cast<const uint16_t*>(P.c.cache.scales + (size_t)max(rr, 0) * (D / 16)) + u0;
@@ -727,7 +720,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
 #pragma unroll
             for (int j = 0; j < 4; ++j) cur[j] = code[j], cs[j] = sc[j];
             if (i + 1 < kGroups) load(i + 1);
-            const uint32_t r = R::kTileRows * w + 8 * i + r8;
+            const uint32_t r = kTileRows * w + 8 * i + r8;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const uint32_t u = u0 + 4 * j;
@@ -766,7 +759,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
           }
 #pragma unroll 1
           for (int i = 0; i < kGroups; ++i) {
-            const int r = R::kTileRows * w + 8 * i + r8, ra = __shfl_sync(0xffffffffu, e0, r & 31),
+            const int r = kTileRows * w + 8 * i + r8, ra = __shfl_sync(0xffffffffu, e0, r & 31),
                       rb = __shfl_sync(0xffffffffu, e1, r & 31), rr = r < 32 ? ra : rb;
             const uint32_t bytes = rr < 0 ? 0u : 16u;
             const uint8_t* src = base + (size_t)max(rr, 0) * (2 * D) + u0 * 16;
@@ -794,7 +787,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         for (uint32_t i = k > nst ? k - nst : 0; i < k; ++i)
           if ((int)(i & 1) == grp) mbar_wait_bounded(&c_full[i & (nst - 1)], (i >> lst) & 1, 1000000);
     }
-  } else if (warp == R::kMma) {
+  } else if (warp == kMmaWarp) {
     // ---- scores: the whole warp runs the loop, one elected lane issues
     const bool leader = elect_one();
     const uint32_t idesc = idesc_bf16(64, kCols), c0 = smem_addr(sC);
@@ -825,7 +818,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
         __syncwarp();
       }
     }
-  } else if (warp == R::kVal) {
+  } else if (warp == kValWarp) {
     // ---- values, likewise
     const bool leader = elect_one();
     const uint32_t idesc = idesc_bf16(128, kCols) | kTransposed, idesc64 = idesc_bf16(64, kCols) | kTransposed;
@@ -891,7 +884,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(raw[i]);
         const int v0 = t * kTile, v1 = min(v0 + kTile, g.s.cnt), v = v0 + 16 * qt + (lane >> 2);
-        bool renew = !ok || (several && t < g.t0 + 2);  // (every token's first row is in the first two tiles)
+        bool renew = !ok;
         uint32_t spoilt = 0;  // bits 0, 1: this thread's rows hold a NaN or infinity that a token must not see
         if (several) {
           // rows that only some of the item's tokens see
@@ -937,7 +930,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
 #pragma unroll
           for (int e = 0; e < 2; ++e) past = fmaxf(past, fmaf(fmaxf(x[4 * i + e], x[4 * i + 2 + e]), sl, -m[2 * i + e]));
         renew = renew || past > kStep;
-        if (t == g.t0) {
+        if (t == g.t0 || (several && t == g.t0 + 1)) {  // (every token's first row is in the first two tiles)
           float low = INFINITY;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -993,9 +986,13 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
 #pragma unroll 4
             for (int i = 0; i < 32; ++i) y = fmaxf(y, col[i * 64 + threadIdx.x]);
             // only the queries that need it: what a query gives does not depend on the others'
-            const bool before = t > g.t0 && (!several || red[128 + threadIdx.x] > kFloor);  // it has seen a row
+            bool before = t > g.t0;  // it has seen a row of the segment
+            if (before && several) {
+              const int tt = colt[threadIdx.x], begin = g.t0 * kTile;
+              const int v = begin < P.sinks ? begin : max(begin, P.window ? tt - P.window + 1 - g.s.jump : 0);
+              before = v < v0 && (v < P.sinks ? v : v + g.s.jump) <= tt;
+            }
             const float m0 = red[threadIdx.x], m1 = y * sl - m0 > kStep || (!before && y > kFloor && y * sl < kLow) ? y * sl : m0;
-            if (several) red[128 + threadIdx.x] = before ? 0.0f : y;
             red[threadIdx.x] = m1;
             red[64 + threadIdx.x] = before ? ex2(m0 - m1) : 1.0f;
           }
@@ -1060,7 +1057,7 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
       // the segment's end: sums over rows, four lanes' of a warp left to the epilogue
 #pragma unroll
       for (int i = 0; i < 8; ++i) l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
-      if (R::kEpi && seg > 1) {
+      if (seg > 1) {
         ok = wait(l_empty, seg - 2);
         if (group_or(1, !ok)) {
           ok = false;
@@ -1075,13 +1072,8 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
 #pragma unroll
         for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(fin + 1024 + 8 * i + c2) = make_float2(m[2 * i], m[2 * i + 1]);
       }
-      if constexpr (R::kEpi) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(l_full);
-      } else {
-        group_sync(1);
-        ok = finish(k - 1, (int)threadIdx.x);
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(l_full);
     }
   }
 
@@ -1089,14 +1081,14 @@ __global__ void __launch_bounds__(Roles<kFp4, kCtas>::kThreads, kCtas)
   __syncthreads();
   if (*abort_flag) {
     if (threadIdx.x == 0) atomicOr(P.flag, 4);
-    if ((warp == R::kMma || warp == R::kVal) && elect_one()) {  // the lanes that issued them
+    if ((warp == kMmaWarp || warp == kValWarp) && elect_one()) {  // the lanes that issued them
       mma_commit(mma_done);
       mbar_wait_bounded(mma_done, 0);
     }
     __syncthreads();
   }
   tc_fence_after();
-  if (warp == R::kMma) tmem_dealloc(tmem, tmem_cols);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, tmem_cols);
 }
 
 // ---- pieces of split items joined.
@@ -1191,46 +1183,40 @@ __global__ void __launch_bounds__(kLanes * kGroups) attention_join_kernel(const 
 }
 
 // ---- host side
-// Stages: as many tiles (a power of two, at most 8) as the shared memory takes: two CTAs an SM up
-// to D = 192 over latents (their tensor memory is 256 columns), else one.
+// Stages: as many tiles (a power of two, at most 8) as the shared memory takes.
 struct Shape {
-  int ctas, stages, smem;
+  int stages, smem;
 };
-Shape attn_shape(int D, bool fp4) {
+Shape attn_shape(int D) {
   Shape s;
-  s.ctas = D <= 192 && !fp4 ? 2 : 1;
   const int chunk = D / 64 * kChunkBytes, rest = 2 * kPBytes + 8 * kStageOut + kAuxBytes + 1024;
-  const int budget = (s.ctas == 2 ? 113 : 227) * 1024 - rest;
   s.stages = 8;
-  while (s.stages > 2 && (s.stages + 1) * chunk > budget) s.stages /= 2;
+  while (s.stages > 2 && (s.stages + 1) * chunk + rest > 227 * 1024) s.stages /= 2;
   s.smem = (s.stages + 1) * chunk + rest;
   return s;
 }
-int attn_slots(int D) { return 2 * current_sm_count() * attn_shape(D, false).ctas; }
+int attn_slots() { return 2 * current_sm_count(); }
 
 }  // namespace
 
 size_t attention_workspace_bytes(int head_dim) {
-  return (size_t)attn_slots(head_dim) * (kCols * (head_dim * sizeof(float) + sizeof(float2)) + sizeof(int2)) + 64;
+  return (size_t)attn_slots() * (kCols * (head_dim * sizeof(float) + sizeof(float2)) + sizeof(int2)) + 64;
 }
 
 cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_t s) {
   auto encode = get_encode();
   if (!encode) return cudaErrorNotSupported;
   const bool fp4 = call.paged && !call.cache.latent;
-  const Shape sh = attn_shape(a->D, fp4);
-  auto* kernel = fp4 ? attention_kernel<true, 1> : sh.ctas == 2 ? attention_kernel<false, 2> : attention_kernel<false, 1>;
-  const int threads = fp4 ? Roles<true, 1>::kThreads : sh.ctas == 2 ? Roles<false, 2>::kThreads : Roles<false, 1>::kThreads;
+  const Shape sh = attn_shape(a->D);
   static std::atomic<unsigned long long> attr{0};
   cudaError_t e = once_per_device(attr, [] {
     const int most = 227 * 1024;
-    cudaError_t r = cudaFuncSetAttribute(attention_kernel<true, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (r == cudaSuccess) r = cudaFuncSetAttribute(attention_kernel<false, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (r == cudaSuccess) r = cudaFuncSetAttribute(attention_kernel<false, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    cudaError_t r = cudaFuncSetAttribute(attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (r == cudaSuccess) r = cudaFuncSetAttribute(attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     return r;
   });
   if (e != cudaSuccess) return e;
-  const int slots = attn_slots(a->D), most_ctas = current_sm_count() * sh.ctas;
+  const int slots = attn_slots(), most_ctas = slots / 2;
   AttnParams P{};
   P.c = call;
   P.H = a->heads;
@@ -1289,7 +1275,10 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  kernel<<<grid, threads, sh.smem, s>>>(mq, mc, P);
+  if (fp4)
+    attention_kernel<true><<<grid, kAttnThreads, sh.smem, s>>>(mq, mc, P);
+  else
+    attention_kernel<false><<<grid, kAttnThreads, sh.smem, s>>>(mq, mc, P);
   a->launches += 1;
   if ((e = cudaGetLastError()) != cudaSuccess || !P.split) return e;
   cudaLaunchAttribute at[1];
