@@ -227,6 +227,19 @@ __device__ __forceinline__ bool group_or(int id, bool p) {
       : "memory");
   return r != 0;
 }
+__device__ __forceinline__ uint64_t l2_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
+      "%4}], [%5], %6;" ::"r"(smem_addr(dst)),
+      "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
 // One lane of a converged warp, the same at every call: what it alone issues stays in uniform
 // registers (an MMA issued under `lane == 0` cost 70 to 126 cycles in descriptor moves, 32 this way).
 __device__ __forceinline__ bool elect_one() {
@@ -305,8 +318,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint32_t* tmem_slot = (uint32_t*)(mma_done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   Segment* ring = (Segment*)(aux + 384);
-  int* work = (int*)(aux + 640);  // split calls: first item, tile, tiles, tile index, end, tiles of a share, shares with one more
-  float* red = (float*)(aux + 704);   // [2][64] references, factors; the scan's sums before
+  int* work = (int*)(aux + 640);  // split calls: tiles of a share, shares with one more
+  float* red = (float*)(aux + 704);   // [2][64] references, factors
   float* fin = red + 128;             // [16][64] sums over rows, [64] references
   float* inv = fin + 1088;            // [64] 1 / sum
   int* colt = (int*)(inv + 64);       // [64] the queries' positions
@@ -356,67 +369,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     for (int b = threadIdx.x; b < P.c.B; b += kAttnThreads) {
       const int n = P.c.lens[b];
       if (n < 0 || n > most) atomicOr(P.flag, 1);
-    }
-  }
-  if (P.split) {
-    // ---- the CTA's share of the call's tiles: every CTA adds up the items' tiles (threads over
-    // contiguous items) and finds its own first one
-    const int per = (P.items + kAttnThreads - 1) / kAttnThreads, lo = min(P.items, per * (int)threadIdx.x),
-              hi = min(P.items, lo + per);
-    int sum = 0, top = 0, all = 0;  // (the host has made sure that the call's tiles fit)
-#pragma unroll 1
-    for (int i = lo; i < hi; ++i) {
-      const int n = tiles_of(seen_rows(P, i));
-      sum += n;
-      top = max(top, n);
-    }
-    int pre = sum;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, pre, o);
-      if (lane >= o) pre += y;
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    }
-    int* ws = (int*)red;  // [warp] sums, then [warp] maxima
-    if (lane == 31) ws[warp] = pre, ws[32 + warp] = top;
-    __syncthreads();
-    {
-      const int y = lane < kAttnThreads / 32 ? ws[lane] : 0;
-      top = lane < kAttnThreads / 32 ? ws[32 + lane] : 0;
-      pre += __reduce_add_sync(0xffffffffu, lane < warp ? y : 0) - sum;  // tiles before this thread's items
-      sum = pre + sum;                                                   // and with them
-      top = __reduce_max_sync(0xffffffffu, top);
-      all = __reduce_add_sync(0xffffffffu, y);
-    }
-    const int total = all;
-    const bool cut = top > kJoinTiles;
-    const int ctas = cut ? min((int)gridDim.x, max(1, total / kMinTiles)) : (int)gridDim.x;
-    // share i begins at each * i + min(i, more)
-    const int each = total / ctas, more = total - each * ctas, i0 = min((int)blockIdx.x, ctas), i1 = min(i0 + 1, ctas);
-    const int a = each * i0 + min(i0, more), e = each * i1 + min(i1, more);
-    if (threadIdx.x == 0) work[0] = P.items, work[1] = 0, work[3] = work[4] = total, work[5] = each, work[6] = more;
-    __syncthreads();
-    // the boundary x: the item it falls in or, without cutting, the first item that starts from it on
-    if ((a >= pre && a < sum) || (e >= pre && e < sum)) {
-      int at = pre;
-#pragma unroll 1
-      for (int item = lo; item < hi; ++item) {
-        const int n = tiles_of(seen_rows(P, item));
-#pragma unroll 1
-        for (int w = 0; w < 2; ++w) {
-          const int x = w ? e : a;
-          if (x < at || x >= at + n) continue;
-          const int tile = x - at;
-          const bool move = !cut && tile > 0;
-          if (w == 0) work[0] = item + move, work[1] = move ? 0 : tile;
-          work[3 + w] = move ? at + n : x;
-        }
-        at += n;
-      }
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      work[2] = work[4] - work[3];
-      if (!P.few) P.record[blockIdx.x] = make_int2(-1, 0);
     }
   }
   tc_fence_before();
@@ -551,7 +503,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       if (g.t0 == 0 && tid == 0) {
         // the item ends in the CTA whose share holds its last tile
-        const int last = g.index + g.tiles - 1, each = work[5], more = work[6], wide = more * (each + 1);
+        const int last = g.index + g.tiles - 1, each = work[0], more = work[1], wide = more * (each + 1);
         const int j = last < wide ? last / (each + 1) : more + (last - wide) / each;
         const int n = j - (int)blockIdx.x + 1;
         P.record[P.few ? g.item : blockIdx.x] = make_int2(P.few ? (int)blockIdx.x : g.item, n);
@@ -561,6 +513,59 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   };
 
   if (warp == kQWarp) {
+    int first_item = blockIdx.x, first_tile = 0, share = 0, first_index = 0;
+    if (P.split) {
+      // ---- the CTA's share of the call's tiles: every CTA's scheduling warp adds up the items' tiles (lanes
+      // over contiguous items; the other roles' instructions arrive meanwhile) and finds its first one
+      const int per = (P.items + 31) / 32, lo = min(P.items, per * lane), hi = min(P.items, lo + per);
+      int sum = 0, top = 0;  // (the host has made sure that the call's tiles fit)
+#pragma unroll 1
+      for (int i = lo; i < hi; ++i) {
+        const int n = tiles_of(seen_rows(P, i));
+        sum += n;
+        top = max(top, n);
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      int pre = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += y;
+      }
+      const int total = __shfl_sync(0xffffffffu, pre, 31);
+      pre -= sum;
+      const bool cut = top > kJoinTiles;
+      const int ctas = cut ? min((int)gridDim.x, max(1, total / kMinTiles)) : (int)gridDim.x;
+      // share i begins at each * i + min(i, more)
+      const int each = total / ctas, more = total - each * ctas, i0 = min((int)blockIdx.x, ctas), i1 = min(i0 + 1, ctas);
+      const int a = each * i0 + min(i0, more), e = each * i1 + min(i1, more);
+      // a boundary x: the item it falls in or, without cutting, the first item that starts from it on
+      int found[2][3] = {{P.items, 0, total}, {P.items, 0, total}};
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w) {
+        const int x = w ? e : a;
+        int item = P.items, tile = 0, start = total;
+        if (x >= pre && x < pre + sum) {
+          int at = pre;
+          item = lo;
+          int n = tiles_of(seen_rows(P, item));
+#pragma unroll 1
+          while (x >= at + n) at += n, n = tiles_of(seen_rows(P, ++item));
+          tile = x - at, start = x;
+          if (!cut && tile > 0) ++item, tile = 0, start = at + n;
+        }
+        const uint32_t who = __ballot_sync(0xffffffffu, x >= pre && x < pre + sum);
+        const int from = who ? __ffs(who) - 1 : 0;
+        found[w][0] = __shfl_sync(0xffffffffu, item, from), found[w][1] = __shfl_sync(0xffffffffu, tile, from);
+        found[w][2] = __shfl_sync(0xffffffffu, start, from);
+      }
+      first_item = found[0][0], first_tile = found[0][1], first_index = found[0][2];
+      share = found[1][2] - found[0][2];
+      if (lane == 0) {
+        work[0] = each, work[1] = more;  // (read by whoever leaves an item's first piece)
+        if (!P.few) P.record[blockIdx.x] = make_int2(-1, 0);
+      }
+    }
     // ---- scheduling and queries (one lane).  A split call's segments are the CTA's share; otherwise
     // items are drawn one at a time from the last (a prompt's longest) on, the CTA's first by its own
     // number: SMs differ in speed, items in length and padding in place.  The CTA that draws the last
@@ -569,8 +574,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // its last are other sequences' or zeros: columns that nothing reads).
     if (lane == 0) {
       const bool split = P.split;
-      int item = split ? work[0] : (int)blockIdx.x, tile = split ? work[1] : 0, drawn = 0;
-      int left = split ? work[2] : 0, index = split ? work[3] : 0;
+      int item = first_item, tile = first_tile, drawn = 0, left = share, index = first_index;
       uint32_t n = 0, loads = 0;
       bool end = false;
       auto draw = [&]() {
@@ -644,6 +648,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // that expand to 64 bytes
     const int r8 = kFp4 ? lane & 7 : (lane >> 3) + 4 * ((lane >> 2) & 1), u0 = kFp4 ? lane >> 3 : lane & 3;
     constexpr int kGroups = kTileRows / 8;
+    // a cache's rows are read once by a call: they are not to drive pieces out of L2
+    const uint64_t policy = P.c.paged ? l2_evict_first() : l2_evict_normal();
     uint32_t k = 0;
     int pending = -1;  // a stage whose copies were issued and not yet handed over
     bool ok = true;
@@ -683,6 +689,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const uint8_t* qrow = (const uint8_t*)(P.c.q + ((size_t)g.s.b * P.c.N * P.H + g.s.f0) * D);
       for (int x = 128 * ((int)threadIdx.x - 32 * kRowWarp); x < g.s.cols * D * 2; x += 128 * 32 * kRowWarps)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(qrow + x));
+      int e0 = 0, e1 = 0;  // lane l's entries l and l + 32 of the tile
+      bool known = false;  // (found when the tile was looked ahead to)
 #pragma unroll 1
       for (int t = g.t0; t < g.t1; ++t, ++k) {
         if ((int)(k & 1) != grp) continue;
@@ -691,8 +699,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (P.test_stall && k == 0) break;  // test of the time-out path: the first tile never comes
 #endif
         const uint32_t dst = smem_addr(sC) + st * stage_bytes;
-        // lane l resolves rows l and l + 32 of the tile
-        const int e0 = entry(t * kTile + lane), e1 = entry(t * kTile + 32 + lane);
+        if (!known) e0 = entry(t * kTile + lane), e1 = entry(t * kTile + 32 + lane);
+        // The group's next tile: its entries, asked into L2 (a half by each warp of the group).  Two stages of
+        // 64 KB a CTA are not enough bytes in flight for HBM's latency.
+        auto look_ahead = [&](int next_t) {
+          known = next_t < g.t1;
+          if (!known) return;
+          e0 = entry(next_t * kTile + lane), e1 = entry(next_t * kTile + 32 + lane);
+          const int row = w ? e1 : e0;
+          const uint8_t* at = kFp4 ? P.c.cache.codes + (size_t)max(row, 0) * (D / 2) : base + (size_t)max(row, 0) * (2 * D);
+          if (row >= 0)
+            for (int x = 0; x < (kFp4 ? D / 2 : 2 * D); x += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + x));
+        };
         if constexpr (kFp4) {
           // codes, expanded into the bf16 operand: a lane takes 32 codes and two scales (half a chunk) of
           // its row at a time; the next eight rows' are on their way while eight are expanded
@@ -741,6 +759,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           }
           hand_over(st);
+          look_ahead(t + 2);
         } else {
           const int e = __shfl_sync(0xffffffffu, e0, 0);
           const bool run = __all_sync(0xffffffffu, e0 >= 0 && e0 == e + lane && e1 == e + 32 + lane) != 0;
@@ -750,11 +769,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (lane == 0) {
               if (w == 0) {
                 mbar_arrive_expect_tx(&c_full[st], (uint32_t)stage_bytes);
-                tma_load_3d(sC + st * stage_bytes, &map_c, 0, e, 0, &c_full[st]);
+                tma_load_3d_hint(sC + st * stage_bytes, &map_c, 0, e, 0, &c_full[st], policy);
               } else {
                 mbar_arrive(&c_full[st]);
               }
             }
+            look_ahead(t + 2);
             continue;
           }
 #pragma unroll 1
@@ -776,6 +796,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             hand_over(pending);
           }
           pending = (int)st;
+          look_ahead(t + 2);
           if (nst == 2) flush();
         }
       }
@@ -1097,41 +1118,76 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // 16 features on; the groups' results are merged like pieces, in order: nothing depends on timing.
 // Few items have many pieces each (16 groups, the item over D / 4 CTAs), many items a few.
 template <int kLanes, int kGroups, int kReps>
-__global__ void __launch_bounds__(kLanes * kGroups) attention_join_kernel(const __grid_constant__ AttnParams P) {
+__global__ void __launch_bounds__(kLanes * kGroups, 1024 / (kLanes * kGroups)) attention_join_kernel(const __grid_constant__ AttnParams P) {
   __shared__ float4 acc[kGroups > 1 ? kGroups : 1][kLanes];
   __shared__ float4 ml[kGroups > 1 ? kGroups : 1][kLanes];
   __shared__ __align__(16) uint16_t tile[kLanes / 4][16];  // queries x 16 features
   griddep_wait();
   const int2 rec = P.record[blockIdx.x];
-  const Seen s = seen_rows(P, kGroups > 1 ? (int)blockIdx.x : max(rec.x, 0));
-  if (rec.x < 0 || s.cols == 0) return;
-  const int n = rec.y, cta = kGroups > 1 ? rec.x : (int)blockIdx.x, j0 = blockIdx.y * kLanes * kReps + threadIdx.x;  // of the piece's 16 D quads of values
+  const int j0 = blockIdx.y * kLanes * kReps + threadIdx.x;  // of the piece's 16 D quads of values
   const int lane = threadIdx.x & 31, grp = threadIdx.y, qt = 8 * (threadIdx.x >> 5) + 2 * (lane & 3);
   const int q0 = 8 * ((j0 >> 5) & 7) - 8 * (int)(threadIdx.x >> 5), q = q0 + qt;  // the CTA's, the thread's first query
-  auto slot = [&](int p) { return 2 * (cta + p) + (p == 0 ? 1 : 0); };
-  auto stats = [&](int p) { return *reinterpret_cast<const float4*>(P.part_ml + slot(p) * kCols + q); };
+  const int most = (int)gridDim.x;  // (with one group of threads a CTA's records: the last CTA has no next)
+  auto stats = [&](int slot) { return *reinterpret_cast<const float4*>(P.part_ml + slot * kCols + q); };
+  auto quad = [&](int slot, int r) {
+    return j0 + r * kLanes < 16 * P.D ? P.part[(size_t)slot * (kCols * P.D / 4) + j0 + r * kLanes] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  };
   float4 y = make_float4(kFloor, 0.0f, kFloor, 0.0f);  // maximum and sum of both queries
-#pragma unroll 4
-  for (int p = grp; p < n; p += kGroups) {
-    const float4 z = stats(p);
-    y.x = fmaxf(y.x, z.x), y.z = fmaxf(y.z, z.z);
-  }
   float4 a[kReps];
+  Seen s;
+  if constexpr (kGroups == 1) {
+    // The first two pieces (a split item has them) are asked for before the record is known: one trip to
+    // L2 instead of three.
+    const int s0 = 2 * blockIdx.x + 1, s1 = 2 * min((int)blockIdx.x + 1, most - 1);
+    const float4 z0 = stats(s0), z1 = stats(s1);
+    float4 o0[kReps], o1[kReps];
 #pragma unroll
-  for (int r = 0; r < kReps; ++r) a[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
-  for (int p = grp; p < n; p += kGroups) {
-    const float4 z = stats(p);
-    const float f0 = ex2(z.x - y.x), f1 = ex2(z.z - y.z);
-    y.y = fmaf(z.y, f0, y.y), y.w = fmaf(z.w, f1, y.w);
-    const float4* src = P.part + (size_t)slot(p) * (kCols * P.D / 4) + j0;
+    for (int r = 0; r < kReps; ++r) o0[r] = quad(s0, r), o1[r] = quad(s1, r);
+    if (rec.x < 0) return;
+    s = seen_rows(P, rec.x);
+    y.x = fmaxf(z0.x, z1.x), y.z = fmaxf(z0.z, z1.z);
+#pragma unroll 1
+    for (int p = 2; p < rec.y; ++p) {
+      const float4 z = stats(2 * (blockIdx.x + p));
+      y.x = fmaxf(y.x, z.x), y.z = fmaxf(y.z, z.z);
+    }
+    const float f0 = ex2(z0.x - y.x), f1 = ex2(z0.z - y.z), g0 = ex2(z1.x - y.x), g1 = ex2(z1.z - y.z);
+    y.y = fmaf(z1.y, g0, z0.y * f0), y.w = fmaf(z1.w, g1, z0.w * f1);
 #pragma unroll
     for (int r = 0; r < kReps; ++r)
-      if (j0 + r * kLanes < 16 * P.D) {
-        const float4 o = src[r * kLanes];
-        a[r].x = fmaf(o.x, f0, a[r].x), a[r].y = fmaf(o.y, f1, a[r].y);
-        a[r].z = fmaf(o.z, f0, a[r].z), a[r].w = fmaf(o.w, f1, a[r].w);
+      a[r] = make_float4(fmaf(o1[r].x, g0, o0[r].x * f0), fmaf(o1[r].y, g1, o0[r].y * f1), fmaf(o1[r].z, g0, o0[r].z * f0),
+                         fmaf(o1[r].w, g1, o0[r].w * f1));
+#pragma unroll 1
+    for (int p = 2; p < rec.y; ++p) {
+      const int slot = 2 * (blockIdx.x + p);
+      const float4 z = stats(slot);
+      const float h0 = ex2(z.x - y.x), h1 = ex2(z.z - y.z);
+      y.y = fmaf(z.y, h0, y.y), y.w = fmaf(z.w, h1, y.w);
+#pragma unroll
+      for (int r = 0; r < kReps; ++r) {
+        const float4 o = quad(slot, r);
+        a[r].x = fmaf(o.x, h0, a[r].x), a[r].y = fmaf(o.y, h1, a[r].y);
+        a[r].z = fmaf(o.z, h0, a[r].z), a[r].w = fmaf(o.w, h1, a[r].w);
       }
+    }
+  } else {
+    s = seen_rows(P, blockIdx.x);
+    if (rec.x < 0 || s.cols == 0) return;
+    auto slot = [&](int p) { return 2 * (rec.x + p) + (p == 0 ? 1 : 0); };
+#pragma unroll 4
+    for (int p = grp; p < rec.y; p += kGroups) {
+      const float4 z = stats(slot(p));
+      y.x = fmaxf(y.x, z.x), y.z = fmaxf(y.z, z.z);
+    }
+    a[0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int p = grp; p < rec.y; p += kGroups) {
+      const float4 z = stats(slot(p)), o = quad(slot(p), 0);
+      const float f0 = ex2(z.x - y.x), f1 = ex2(z.z - y.z);
+      y.y = fmaf(z.y, f0, y.y), y.w = fmaf(z.w, f1, y.w);
+      a[0].x = fmaf(o.x, f0, a[0].x), a[0].y = fmaf(o.y, f1, a[0].y);
+      a[0].z = fmaf(o.z, f0, a[0].z), a[0].w = fmaf(o.w, f1, a[0].w);
+    }
   }
   if constexpr (kGroups > 1) {
     acc[grp][threadIdx.x] = a[0], ml[grp][threadIdx.x] = y;
@@ -1285,14 +1341,14 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = P.few ? dim3(P.items, a->D / 4) : dim3(grid, (a->D + 127) / 128);
+  cfg.gridDim = P.few ? dim3(P.items, a->D / 4) : dim3(grid, a->D / 64);
   cfg.blockDim = P.few ? dim3(64, 16) : dim3(256, 1);
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   a->launches += 1;
   return P.few ? cudaLaunchKernelEx(&cfg, attention_join_kernel<64, 16, 1>, P)
-             : cudaLaunchKernelEx(&cfg, attention_join_kernel<256, 1, 8>, P);
+             : cudaLaunchKernelEx(&cfg, attention_join_kernel<256, 1, 4>, P);
 }
 
 }  // namespace csa
