@@ -212,18 +212,20 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t wait_ns) {
   return mbar_wait(bar, parity, abort_flag, wait_ns);
 }
-// A barrier of eight warps (1: softmax, 2: epilogue); group_or gives every thread whether any passed
+// A barrier of some warps (1: softmax, 2: epilogue); group_or gives every thread whether any passed
 // true.
-constexpr int kWorkers = 8, kGroupThreads = 256;
+constexpr int kSoftWarps = 8;
+template <int kWarps = kSoftWarps>
 __device__ __forceinline__ void group_sync(int id) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kGroupThreads) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(32 * kWarps) : "memory");
 }
+template <int kWarps = kSoftWarps>
 __device__ __forceinline__ bool group_or(int id, bool p) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)p), "r"(id), "n"(kGroupThreads)
+      : "r"((uint32_t)p), "r"(id), "n"(32 * kWarps)
       : "memory");
   return r != 0;
 }
@@ -283,15 +285,25 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t scale2) {
 // take alternate tiles (one group's tile can be in flight while the other waits for its stage).
 // One CTA an SM at every D: two of half the warps shared an SM up to D = 192 (their softmax warps
 // reading their own O^T) and took 118 us where this takes 66 (2 x 1777 tokens, D 128, window 512).
-constexpr int kEpiWarp = 8, kMmaWarp = 16, kValWarp = 17, kQWarp = 18, kRowWarp = 19;
-constexpr int kRowWarps = 4, kRowGroup = kRowWarps / 2;  // two warps bring a tile
-constexpr int kTileRows = kTile / kRowGroup;             // 32 rows each
-constexpr int kAttnThreads = 32 * (kRowWarp + kRowWarps);
+// Codes need more warps to expand them (four a tile; with two, 16 expanding instructions a code pair and
+// warp took twice the time of the tile's MMAs) and give up half of the epilogue's.
+constexpr int kEpiWarp = 8;
+constexpr int kAttnThreads = 32 * 23;
+template <bool kFp4>
+struct Roles {
+  static constexpr int kEpiWarps = kFp4 ? 4 : 8;
+  static constexpr int kMma = kEpiWarp + kEpiWarps, kVal = kMma + 1, kQ = kMma + 2, kRow = kMma + 3;
+  static constexpr int kRowWarps = kAttnThreads / 32 - kRow, kRowGroup = kRowWarps / 2;  // a group brings a tile
+  static constexpr int kTileRows = kTile / kRowGroup;                                   // of which a warp these
+};
 
 template <bool kFp4>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_c,
                      const __grid_constant__ AttnParams P) {
+  using R = Roles<kFp4>;
+  constexpr int kEpiWarps = R::kEpiWarps, kMmaWarp = R::kMma, kValWarp = R::kVal, kQWarp = R::kQ, kRowWarp = R::kRow;
+  constexpr int kRowWarps = R::kRowWarps, kRowGroup = R::kRowGroup, kTileRows = R::kTileRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const int D = P.D, chunks = D / 64;
@@ -342,7 +354,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kWorkers);
+      mbar_init(&p_full[i], kSoftWarps);
       mbar_init(&pv_done[i], 1);
     }
     for (int i = 0; i < kRing; ++i) {
@@ -351,9 +363,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&o_empty[i], kWorkers);
-    mbar_init(l_full, kWorkers);
-    mbar_init(l_empty, kWorkers);
+    for (int i = 0; i < 4; ++i) mbar_init(&o_empty[i], kEpiWarps);
+    mbar_init(l_full, kSoftWarps);
+    mbar_init(l_empty, kEpiWarps);
     mbar_init(mma_done, 2);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -389,15 +401,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     return g.t1 > 0;
   };
 
-  // ---- an item's end, by eight warps, two of each of O^T's lane quarters (warp % 4: they
+  // ---- an item's end, by the epilogue's warps, one or two of each of O^T's lane quarters (warp % 4; two
   // share its columns or halves): the sums over rows in `fin`, O^T (complete with tile kl) scaled to
   // out, or left as a piece.  A block of 128 features is given back to the MMAs as soon as it has
   // been read.  False after an abort.
   auto finish = [&](uint32_t kl, int tid) -> bool {
+    constexpr int kTwo = kEpiWarps / 4;
     const int w = warp & 3, half = tid >> 7;
     bool ok = wait(l_full, seg - 1);
     ok = ok && wait(&pv_done[kl & 1], kl >> 1);
-    if (group_or(2, !ok)) return false;
+    if (group_or<kEpiWarps>(2, !ok)) return false;
     tc_fence_after();
     const bool whole = g.t0 == 0 && g.t1 == g.tiles;
     // a piece: slot 0 of the CTA for its first segment's, 1 for its last's (an item's first piece)
@@ -419,7 +432,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         P.part_ml[slot * kCols + tid] = make_float2(l == 0.0f ? kFloor : m, l);  // (no row: no reference either)
       }
     }
-    group_sync(2);
+    group_sync<kEpiWarps>(2);
     if (lane == 0) mbar_arrive(l_empty);
     auto give_back = [&](int block) {
       tc_fence_before();
@@ -436,7 +449,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tmem_ld_half(base + 32 * half, o[0]);
       tmem_ld_half(base + 32 * half + (16u << 16), o[1]);
 #pragma unroll 1
-      for (int step = half; step < steps; step += 2) {
+      for (int step = half; step < steps; step += kTwo) {
         const int x = step & ~1, c = step & 1;
         const bool full = x + 1 < chunks;
         float2 f[4];
@@ -454,9 +467,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               v[i][h][j] = bf16x2(__uint_as_float(o[h][4 * q + 2 * (j & 1)]) * f[q].x,
                                   __uint_as_float(o[h][4 * q + 2 * (j & 1) + 1]) * f[q].y);
             }
-        give_back(step >> 1);
-        if (step + 2 < steps) {
-          const uint32_t at = base + 32 * (step + 2);  // 64 columns a block of 128 features
+        if (kTwo == 2 || c == 1) give_back(step >> 1);
+        if (step + kTwo < steps) {
+          const uint32_t at = base + 32 * (step + kTwo);  // 64 columns a block of 128 features
           tmem_ld_half(at, o[0]);
           tmem_ld_half(at + (16u << 16), o[1]);
         }
@@ -490,7 +503,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     } else {
       float4* dst = P.part + (size_t)slot * (kCols * D / 4) + w * 256 + lane;
 #pragma unroll 1
-      for (int x = half; x < ((chunks + 1) & ~1); x += 2) {  // half x % 2 of 16 lanes a warp of a block
+      for (int x = half; x < ((chunks + 1) & ~1); x += kTwo) {  // half x % 2 of 16 lanes a warp of a block
         if (x < chunks) {
         uint32_t o[32];
         tmem_ld_frag(base + (x >> 1) * kCols + ((uint32_t)(16 * (x & 1)) << 16), o);
@@ -499,7 +512,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           dst[(x * 32 + i) * 32] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         }
-        give_back(x >> 1);
+        if (kTwo == 2 || (x & 1)) give_back(x >> 1);
       }
       if (g.t0 == 0 && tid == 0) {
         // the item ends in the CTA whose share holds its last tile
@@ -633,7 +646,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         while (*abort_flag && item < P.items) item = drawn, drawn = item < P.items ? draw() : item;
       if (*abort_flag && loads > 0) mbar_wait_bounded(q_full, (loads - 1) & 1);
     }
-  } else if (warp >= kEpiWarp && warp < kEpiWarp + kWorkers) {
+  } else if (warp >= kEpiWarp && warp < kMmaWarp) {
     uint32_t k = 0;
     while (next()) {
       k += g.t1 - g.t0;
@@ -706,7 +719,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           known = next_t < g.t1;
           if (!known) return;
           e0 = entry(next_t * kTile + lane), e1 = entry(next_t * kTile + 32 + lane);
-          const int row = w ? e1 : e0;
+          const int row = w == 0 ? e0 : w == 1 ? e1 : -1;
           const uint8_t* at = kFp4 ? P.c.cache.codes + (size_t)max(row, 0) * (D / 2) : base + (size_t)max(row, 0) * (2 * D);
           if (row >= 0)
             for (int x = 0; x < (kFp4 ? D / 2 : 2 * D); x += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + x));
