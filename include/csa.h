@@ -424,8 +424,9 @@ void csa_attention_destroy(csa_attention* a);
  *  y             [rows][dim] bf16 dev or NULL: e.g. the compressor's x
  *  q             [rows][dim] e4m3 dev: round to nearest even, saturating at 448
  *  scales        [rows][dim / scale_block] f32, or u8 with scale_block 32, dev
- * The quotient is an IEEE f32 division.  A row with a NaN or an infinity gives what the formula
- * gives (NaN; a NaN block has a NaN scale, e8m0 byte 255).
+ * n / a is the f32 product of n with the f32 reciprocal of a (one division a block).  A row with
+ * a NaN or an infinity gives what the formula gives (NaN; a NaN block has a NaN scale, e8m0 byte
+ * 255).
  * Requirements: dim a multiple of scale_block and of 32, at most 16384; arrays 16-byte aligned
  * (scales 4).  rows may be 0 (nothing is enqueued). */
 int csa_rmsnorm_residual_q8(const uint16_t* x, const uint16_t* residual, const float* gain, int64_t rows, int dim,
