@@ -1264,12 +1264,11 @@ Shape attn_shape(int D) {
   s.smem = (s.stages + 1) * chunk + rest;
   return s;
 }
-int attn_slots() { return 2 * current_sm_count(); }
 
 }  // namespace
 
 size_t attention_workspace_bytes(int head_dim) {
-  return (size_t)attn_slots() * (kCols * (head_dim * sizeof(float) + sizeof(float2)) + sizeof(int2)) + 64;
+  return 2 * (size_t)current_sm_count() * (kCols * (head_dim * sizeof(float) + sizeof(float2)) + sizeof(int2)) + 64;
 }
 
 cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_t s) {
@@ -1285,7 +1284,7 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
     return r;
   });
   if (e != cudaSuccess) return e;
-  const int slots = attn_slots(), most_ctas = slots / 2;
+  const int slots = 2 * a->sms, most_ctas = a->sms;
   AttnParams P{};
   P.c = call;
   P.H = a->heads;

@@ -97,6 +97,7 @@ int csa_attention_create(int heads, int head_dim, int window, int sinks, float s
   a->sinks = window ? sinks : 0;
   a->scale = scale > 0.0f ? scale : (float)(1.0 / std::sqrt((double)head_dim));
   cudaError_t e = cudaGetDevice(&a->device);
+  a->sms = csa::current_sm_count();
   if (e == cudaSuccess) e = cudaMalloc((void**)&a->dev_flag, sizeof(int));
   if (e == cudaSuccess) e = cudaMalloc((void**)&a->workspace, csa::attention_workspace_bytes(head_dim));
   if (e == cudaSuccess) e = cudaMemset(a->dev_flag, 0, sizeof(int));

@@ -34,7 +34,7 @@ cudaError_t launch_rmsnorm_residual_q8(const uint16_t* x, const uint16_t* residu
 }  // namespace csa
 
 struct csa_attention {
-  int heads, D, window, sinks, device;
+  int heads, D, window, sinks, device, sms;
   float scale;
   int* dev_flag;       // device-side error flag
   uint8_t* workspace;  // partial results of split sequences

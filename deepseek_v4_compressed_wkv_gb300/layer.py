@@ -17,6 +17,7 @@ belong to that stream, and those passed in are kept for it.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -24,7 +25,9 @@ from . import CSAError, Out, _check, load_library
 
 __all__ = ["Attention", "PagedCache", "rmsnorm_residual_q8"]
 
+_empty, _empty_like = torch.empty, torch.empty_like
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_current_device = torch.cuda.current_device
 _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 
@@ -114,7 +117,7 @@ class PagedCache:
         """Writes entries (a compressor call's outputs, [B, G, ..], or [B, ..] for one each) of
         sequence b to indices first[b] .. of its pages, where mask[b] is not 0.  page_table int32
         [B, max_pages], first int32 [B], mask u8 [B] or None."""
-        dev = torch.cuda.current_device()
+        dev = _current_device()
         if self.device != dev:
             raise CSAError(f"the cache is on cuda:{self.device}, but the current CUDA device is cuda:{dev}")
         B = first.shape[0]
@@ -195,7 +198,7 @@ class Attention:
         B, N = q.shape[0], q.shape[1]
         if start_pos < 0 or start_pos + N > kv.shape[1]:
             raise CSAError(f"start_pos {start_pos} must be >= 0 and start_pos + {N} at most kv's {kv.shape[1]} rows")
-        dev = torch.cuda.current_device()
+        dev = _current_device()
         shape, lshape = (B, N, self.heads, self.head_dim), (B, N, self.heads)
         qp = _want("q", q, _BF16, shape, dev)
         kp = _want("kv", kv, _BF16, (B, kv.shape[1], self.head_dim), dev)
@@ -209,13 +212,16 @@ class Attention:
     def _outputs(self, q, out, lse, shape, lshape, dev, stream, used):
         """(pointer, out, pointer, lse, stream handle) of a call."""
         if stream is None:
-            out = torch.empty_like(q) if out is None else out
-            lse = torch.empty(lshape, dtype=_F32, device=q.device) if lse is None else lse
             s = _raw_stream(dev)
+            if out is None and lse is None:  # (nothing of the caller's to check)
+                out, lse = _empty_like(q), _empty(lshape, dtype=_F32, device=q.device)
+                return out.data_ptr(), out, lse.data_ptr(), lse, s
+            out = _empty_like(q) if out is None else out
+            lse = _empty(lshape, dtype=_F32, device=q.device) if lse is None else lse
         else:
             make, s = _Here(stream, used), stream.cuda_stream
-            out = make(torch.empty_like, q) if out is None else out
-            lse = make(torch.empty, lshape, dtype=_F32, device=q.device) if lse is None else lse
+            out = make(_empty_like, q) if out is None else out
+            lse = make(_empty, lshape, dtype=_F32, device=q.device) if lse is None else lse
         return _want("out", out, _BF16, shape, dev), out, _want("lse", lse, _F32, lshape, dev), lse, s
 
     def decode(self, q, cache: PagedCache, page_table, lens, out=None, lse=None, stream=None):
@@ -225,7 +231,7 @@ class Attention:
         if q.dim() != 3 or page_table.dim() != 2:
             raise CSAError("q must be [B, heads, head_dim] and page_table [B, max_pages]")
         B = q.shape[0]
-        dev = torch.cuda.current_device()
+        dev = _current_device()
         if cache.device != dev:
             raise CSAError(f"the cache is on cuda:{cache.device}, but the current CUDA device is cuda:{dev}")
         shape, lshape = (B, self.heads, self.head_dim), (B, self.heads)
@@ -248,10 +254,6 @@ class Attention:
         return _check(self._lib.csa_attention_status(self._h, s), "csa_attention_status")
 
 
-def _call(make, *args, **kw):
-    return make(*args, **kw)
-
-
 def rmsnorm_residual_q8(x, residual, gain, eps: float = 1e-6, scale_block: int = 128, y: bool = True, inplace: bool = False,
                         stream=None) -> dict:
     """x bf16 [.., dim] plus residual (or None), normalised by its root mean square with gain f32 [dim].
@@ -265,19 +267,16 @@ def rmsnorm_residual_q8(x, residual, gain, eps: float = 1e-6, scale_block: int =
         raise CSAError(f"the last dimension must be a multiple of {128 if scale_block == 128 else 32}, got {dim}")
     if inplace and residual is None:
         raise CSAError("inplace writes over a residual: none was given")
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     xp = _want("x", x, _BF16, x.shape, dev)
     rp = None if residual is None else _want("residual", residual, _BF16, x.shape, dev)
     gp = _want("gain", gain, _F32, (dim,), dev)
-    if stream is None:
-        make, s = _call, _raw_stream(dev)
-    else:
-        make, s = _Here(stream, (x, residual, gain)), stream.cuda_stream
-    total = x if residual is None else residual if inplace else make(torch.empty_like, x)
-    yt = make(torch.empty_like, x) if y else None
-    q = make(torch.empty_like, x, dtype=_E4M3)
-    scales = make(torch.empty, (*x.shape[:-1], dim // (scale_block or dim)), dtype=_E8M0 if scale_block == 32 else _F32,
-                  device=x.device)
+    make, s = (None, _raw_stream(dev)) if stream is None else (_Here(stream, (x, residual, gain)), stream.cuda_stream)
+    empty, like = (_empty, _empty_like) if make is None else (functools.partial(make, _empty), functools.partial(make, _empty_like))
+    total = x if residual is None else residual if inplace else like(x)
+    yt = like(x) if y else None
+    q = like(x, dtype=_E4M3)
+    scales = empty((*x.shape[:-1], dim // (scale_block or dim)), dtype=_E8M0 if scale_block == 32 else _F32, device=x.device)
     rc = load_library().csa_rmsnorm_residual_q8(xp, rp, gp, x.numel() // dim, dim, eps, scale_block,
                                                 None if residual is None else total.data_ptr(),
                                                 None if yt is None else yt.data_ptr(), q.data_ptr(), scales.data_ptr(), s)
