@@ -25,7 +25,7 @@
 // come by 16-byte cp.async, which takes any page size and leaves hidden rows out (zeros) at the rate
 // of tiled TMA boxes (760 cycles a tile from L2, against 8010 for four-row TMA gathers).
 //
-// Work is cut by tiles: the call's tiles, in item order, are divided evenly over the CTAs, so ragged
+// Work is cut by tiles: the call's tiles (and one's time for each item), in item order, are divided evenly over the CTAs, so ragged
 // lengths and few long sequences fill the GPU alike; an item cut by a CTA boundary leaves partial
 // (m, l, O) pieces in the workspace, which a second kernel joins.  Where no item is longer than
 // kJoinTiles tiles the boundaries are moved to item starts instead: the imbalance costs less than
@@ -120,11 +120,15 @@ __device__ __forceinline__ int tiles_of(const Seen& s) {
   return s.cols == 0 ? 0 : max(1, (s.cnt + kTile - 1) / kTile);  // a sequence without entries still has its output
 }
 
+// What an item costs in a split call's shares, in tiles: a CTA takes about as long over changing to an
+// item (its queries' copy, the epilogue) as over a tile.
+__device__ __forceinline__ int units_of(int tiles) { return tiles == 0 ? 0 : tiles + 1; }
+
 // A run of tiles of one item, as the scheduling warp hands it to the others through a ring of slots.
 struct __align__(16) Segment {
   Seen s;
   int item, t0, t1, tiles;  // tiles [t0, t1) of the item's; t1 0: no more segments
-  int index;                // tile t0's number among the call's tiles (split calls)
+  int index;                // units of the call before this segment (split calls)
 };
 static_assert(sizeof(Segment) == 48, "a ring slot");
 constexpr int kRing = 4;
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint32_t* tmem_slot = (uint32_t*)(mma_done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   Segment* ring = (Segment*)(aux + 384);
-  int* work = (int*)(aux + 640);  // split calls: tiles of a share, shares with one more
+  int* work = (int*)(aux + 640);  // split calls: units of a share, shares with one more
   float* red = (float*)(aux + 704);   // [2][64] references, factors
   float* fin = red + 128;             // [16][64] sums over rows, [64] references
   float* inv = fin + 1088;            // [64] 1 / sum
@@ -374,6 +378,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const uint32_t oc = (uint32_t)((D + 127) / 128) * kCols;  // columns of O^T; two score buffers follow
   const uint32_t tmem_cols = oc + 2 * kCols <= 256 ? 256 : 512;
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, tmem_cols);
+  griddep_wait();  // what the launches before this one wrote and read
   griddep_launch_dependents();
 
   if (blockIdx.x == 0 && P.c.lens) {  // lengths out of range are taken as the nearest end
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       if (g.t0 == 0 && tid == 0) {
         // the item ends in the CTA whose share holds its last tile
-        const int last = g.index + g.tiles - 1, each = work[0], more = work[1], wide = more * (each + 1);
+        const int last = g.index + g.tiles, each = work[0], more = work[1], wide = more * (each + 1);
         const int j = last < wide ? last / (each + 1) : more + (last - wide) / each;
         const int n = j - (int)blockIdx.x + 1;
         P.record[P.few ? g.item : blockIdx.x] = make_int2(P.few ? (int)blockIdx.x : g.item, n);
@@ -528,14 +533,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (warp == kQWarp) {
     int first_item = blockIdx.x, first_tile = 0, share = 0, first_index = 0;
     if (P.split) {
-      // ---- the CTA's share of the call's tiles: every CTA's scheduling warp adds up the items' tiles (lanes
-      // over contiguous items; the other roles' instructions arrive meanwhile) and finds its first one
+      // ---- the CTA's share of the call's units: every CTA's scheduling warp adds up the items' (lanes over
+      // contiguous items; the other roles' instructions arrive meanwhile) and finds its first one
       const int per = (P.items + 31) / 32, lo = min(P.items, per * lane), hi = min(P.items, lo + per);
-      int sum = 0, top = 0;  // (the host has made sure that the call's tiles fit)
+      int sum = 0, top = 0;  // (the host has made sure that the call's units fit)
 #pragma unroll 1
       for (int i = lo; i < hi; ++i) {
         const int n = tiles_of(seen_rows(P, i));
-        sum += n;
+        sum += units_of(n);
         top = max(top, n);
       }
       top = __reduce_max_sync(0xffffffffu, top);
@@ -561,10 +566,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (x >= pre && x < pre + sum) {
           int at = pre;
           item = lo;
-          int n = tiles_of(seen_rows(P, item));
+          int n = units_of(tiles_of(seen_rows(P, item)));
 #pragma unroll 1
-          while (x >= at + n) at += n, n = tiles_of(seen_rows(P, ++item));
-          tile = x - at, start = x;
+          while (x >= at + n) at += n, n = units_of(tiles_of(seen_rows(P, ++item)));
+          // the unit of the change goes with the first tile
+          tile = max(0, x - at - 1), start = tile ? x : at;
           if (!cut && tile > 0) ++item, tile = 0, start = at + n;
         }
         const uint32_t who = __ballot_sync(0xffffffffu, x >= pre && x < pre + sum);
@@ -596,8 +602,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         return (int)gridDim.x + t;
       };
       auto advance = [&](const Segment& a) {
-        left -= a.t1 - a.t0;
-        index += a.t1 - a.t0;
+        const int units = a.t0 == 0 ? units_of(a.t1) : a.t1 - a.t0;
+        left -= units;
+        index += units;
         tile = 0;
         if (split) {
           ++item;
@@ -618,7 +625,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           a.s = seen_rows(P, a.item);
           a.tiles = tiles_of(a.s);
           a.t0 = tile;
-          a.t1 = split ? min(a.tiles, tile + left) : a.tiles;
+          a.t1 = split ? min(a.tiles, tile == 0 ? left - 1 : tile + left) : a.tiles;
           a.index = index;
           more = a.t1 > tile;
           if (more) break;
@@ -1314,7 +1321,7 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
   if (a->window && most > window) most = window;
   // (a prompt with several items a CTA is not: drawing them, the longest first, balances as well)
   P.split = most > (long long)kJoinTiles * kTile && (call.paged || P.items < 4 * most_ctas);
-  const long long longest = most > kTile ? (most + kTile - 1) / kTile : 1, tiles = P.items * longest;
+  const long long longest = most > kTile ? (most + kTile - 1) / kTile : 1, tiles = P.items * (longest + 1);
   if (P.split && tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
   const long long shares = P.split ? tiles : P.items;
   const int grid = (int)(shares < most_ctas ? shares : most_ctas);
@@ -1343,21 +1350,23 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  if (fp4)
-    attention_kernel<true><<<grid, kAttnThreads, sh.smem, s>>>(mq, mc, P);
-  else
-    attention_kernel<false><<<grid, kAttnThreads, sh.smem, s>>>(mq, mc, P);
-  a->launches += 1;
-  if ((e = cudaGetLastError()) != cudaSuccess || !P.split) return e;
+  // Both kernels may be set up while the launch before them ends: what they read and write waits for it.
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = P.few ? dim3(P.items, a->D / 4) : dim3(grid, a->D / 64);
-  cfg.blockDim = P.few ? dim3(64, 16) : dim3(256, 1);
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kAttnThreads);
+  cfg.dynamicSmemBytes = sh.smem;
+  a->launches += 1;
+  e = fp4 ? cudaLaunchKernelEx(&cfg, attention_kernel<true>, mq, mc, P) : cudaLaunchKernelEx(&cfg, attention_kernel<false>, mq, mc, P);
+  if (e != cudaSuccess || !P.split) return e;
+  cfg.dynamicSmemBytes = 0;
+  cfg.gridDim = P.few ? dim3(P.items, a->D / 4) : dim3(grid, a->D / 64);
+  cfg.blockDim = P.few ? dim3(64, 16) : dim3(256, 1);
   a->launches += 1;
   return P.few ? cudaLaunchKernelEx(&cfg, attention_join_kernel<64, 16, 1>, P)
              : cudaLaunchKernelEx(&cfg, attention_join_kernel<256, 1, 4>, P);
