@@ -932,27 +932,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int begin = max(v0, P.sinks);
           if ((v1 - 1 < P.sinks ? v1 - 1 : v1 - 1 + g.s.jump) > g.s.tlo ||
               (P.window && begin < v1 && begin + g.s.jump <= g.s.thi - P.window)) {
+            int2 tc[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc[i] = *reinterpret_cast<const int2*>(colt + 8 * i + c2);
+            float odd = 0.0f;  // NaN if any score is not finite
+#pragma unroll
+            for (int i = 0; i < 16; ++i) odd = fmaf(x[i], 0.0f, odd);
+            const bool rare = __any_sync(0xffffffffu, odd != 0.0f);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+              // a row is seen by the tokens of its position and the next `reach`
               const int vv = v + 8 * h, j = vv < P.sinks ? vv : vv + g.s.jump;
-              const int low = P.window && vv >= P.sinks ? j + P.window : 0x7fffffff;  // hidden from there on
+              const uint32_t reach = P.window && vv >= P.sinks ? P.window : 0x7fffffffu;
+              if (rare) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int2 tc = *reinterpret_cast<const int2*>(colt + 8 * i + c2);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int tt = e ? tc.y : tc.x;
-                  float& y = x[4 * i + 2 * h + e];
+                for (int i = 0; i < 8; ++i) {
+                  float& y = x[4 * (i >> 1) + 2 * h + (i & 1)];
                   // a score of -inf is a row with an infinity: NaN for a token that sees it
-                  if (j > tt || tt >= low) {
-                    if (!(fabsf(y) < INFINITY)) spoilt |= 1u << h;
-                    y = -INFINITY;
-                  } else if (y == -INFINITY) {
-                    y = __int_as_float(0x7fffffff);
+                  if ((uint32_t)((i & 1 ? tc[i >> 1].y : tc[i >> 1].x) - j) < reach) {
+                    if (y == -INFINITY) y = __int_as_float(0x7fffffff);
+                  } else if (!(fabsf(y) < INFINITY)) {
+                    spoilt |= 1u << h;
                   }
                 }
+                if (vv >= g.s.cnt) spoilt &= ~(1u << h);
               }
-              if (vv >= g.s.cnt) spoilt &= ~(1u << h);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if ((uint32_t)((i & 1 ? tc[i >> 1].y : tc[i >> 1].x) - j) >= reach) x[4 * (i >> 1) + 2 * h + (i & 1)] = -INFINITY;
             }
             renew = renew || spoilt;
           }
