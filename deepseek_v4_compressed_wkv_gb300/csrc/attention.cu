@@ -76,13 +76,14 @@ struct AttnParams {
   float2* part_ml;   // (maximum, sum) of each piece and query [2 * grid][64]
   int2* record;      // per CTA: (item, pieces) of an item whose first piece it made, or (-1, 0); per
                      // item with few of them: (CTA of the first piece, pieces), or (-1, 0)
+  int ctas;          // of the kernel that leaves pieces
   bool few;
   int log_stages;
   bool split;        // items may be cut (the join kernel follows); else they are drawn from `ticket`
   int* ticket;       // items drawn beyond each CTA's first; 0 between calls
 #ifdef CSA_DEBUG_BOUNDS
   uint64_t wait_ns;  // the time-out test shortens the waits
-  int test_stall;    // and leaves out each CTA's last tile
+  int test_stall;    // and leaves out each CTA's first tile
 #endif
 };
 
@@ -1150,7 +1151,9 @@ __global__ void __launch_bounds__(kLanes * kGroups, 1024 / (kLanes * kGroups)) a
   __shared__ float4 ml[kGroups > 1 ? kGroups : 1][kLanes];
   __shared__ __align__(16) uint16_t tile[kLanes / 4][16];  // queries x 16 features
   griddep_wait();
-  const int2 rec = P.record[blockIdx.x];
+  int2 rec = P.record[blockIdx.x];
+  // (after a wait that ran out a record may be an earlier call's: no index comes from one that does not fit)
+  if (kGroups == 1 ? rec.x >= P.items || rec.y > P.ctas - (int)blockIdx.x : rec.x < 0 || rec.y > P.ctas - rec.x) rec.x = -1;
   const int j0 = blockIdx.y * kLanes * kReps + threadIdx.x;  // of the piece's 16 D quads of values
   const int lane = threadIdx.x & 31, grp = threadIdx.y, qt = 8 * (threadIdx.x >> 5) + 2 * (lane & 3);
   const int q0 = 8 * ((j0 >> 5) & 7) - 8 * (int)(threadIdx.x >> 5), q = q0 + qt;  // the CTA's, the thread's first query
@@ -1285,6 +1288,18 @@ size_t attention_workspace_bytes(int head_dim) {
   return 2 * (size_t)current_sm_count() * (kCols * (head_dim * sizeof(float) + sizeof(float2)) + sizeof(int2)) + 64;
 }
 
+// The units (see units_of) that a call whose items may be cut can have at most; 0 where none is cut.
+long long attention_units(const csa_attention* a, const AttnCall& call) {
+  // the longest range of rows that this call can have decides whether items may be cut
+  const long long items = call.B * (((long long)call.N * a->heads + kCols - 1) / kCols);
+  long long most = call.paged ? (long long)call.max_pages * call.cache.page_size : (long long)call.start + call.N;
+  const long long window = (long long)a->window + a->sinks + (kCols - 1) / a->heads + 1;
+  if (a->window && most > window) most = window;
+  // (a prompt with several items a CTA is not: drawing them, the longest first, balances as well)
+  if (most <= (long long)kJoinTiles * kTile || (!call.paged && items >= 4LL * a->sms)) return 0;
+  return items * ((most + kTile - 1) / kTile + 1);
+}
+
 cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_t s) {
   auto encode = get_encode();
   if (!encode) return cudaErrorNotSupported;
@@ -1298,7 +1313,7 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
     return r;
   });
   if (e != cudaSuccess) return e;
-  const int slots = 2 * a->sms, most_ctas = a->sms;
+  const int slots = 2 * a->sms;
   AttnParams P{};
   P.c = call;
   P.H = a->heads;
@@ -1322,17 +1337,13 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
   P.test_stall = getenv("CSA_TEST_STALL_LAST_STAGE") != nullptr;
   P.wait_ns = P.test_stall ? 200000000ull : kWaitNs;
 #endif
-  // the longest range of rows that this call can have decides whether items may be cut
-  long long most = call.paged ? (long long)call.max_pages * call.cache.page_size : (long long)call.start + call.N;
-  const long long window = (long long)a->window + a->sinks + kCols / a->heads;
-  if (a->window && most > window) most = window;
-  // (a prompt with several items a CTA is not: drawing them, the longest first, balances as well)
-  P.split = most > (long long)kJoinTiles * kTile && (call.paged || P.items < 4 * most_ctas);
-  const long long longest = most > kTile ? (most + kTile - 1) / kTile : 1, tiles = P.items * (longest + 1);
-  if (P.split && tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const long long shares = P.split ? tiles : P.items;
-  const int grid = (int)(shares < most_ctas ? shares : most_ctas);
-  P.few = P.items * 8 <= grid;
+  const long long units = attention_units(a, call);
+  P.split = units > 0;
+  if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long shares = P.split ? units : P.items;
+  const int grid = (int)(shares < a->sms ? shares : a->sms);
+  P.ctas = grid;
+  P.few = P.items * 8LL <= grid;
   CUtensorMap mq;
   {
     cuuint64_t dims[2] = {(cuuint64_t)a->D, (cuuint64_t)call.B * call.N * a->heads};

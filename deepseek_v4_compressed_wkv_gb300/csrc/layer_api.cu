@@ -139,6 +139,8 @@ int csa_attention_prefill(csa_attention* a, const uint16_t* q, const uint16_t* k
   c.N = N;
   c.start = start_pos;
   c.kv_rows = kv_rows;
+  if (csa::attention_units(a, c) > 0x7fffffffLL)
+    return fail(CSA_ERR_ARG, "%s: too many tiles of 64 rows (items of 64 queries times rows / 64): 2^31 or more", what);
   CSA_CUDA(csa::launch_attention(a, c, (cudaStream_t)stream), "attention launch");
   return CSA_OK;
 }
@@ -153,7 +155,7 @@ int csa_attention_decode(csa_attention* a, const uint16_t* q, const csa_cache* c
     return fail(CSA_ERR_ARG, "%s: the cache holds %d features, the handle %d", what, cache->head_dim, a->D);
   if (!cache->latent && cache->fp4 != 1)
     return fail(CSA_ERR_ARG, "%s: codes must have e4m3 scales per 16 (fp4 = 1)", what);
-  if (cache->latent && cache->pages > 0x7ffffffeLL / cache->page_size)
+  if (cache->pages > 0x7ffffffeLL / cache->page_size)
     return fail(CSA_ERR_ARG, "%s: the cache's entries must number less than 2^31 - 1", what);
   if (B < 1 || (long long)B * a->heads > 0x7fffffffLL) return fail(CSA_ERR_ARG, "%s: B (%d) must be >= 1", what, B);
   if (max_pages < 0 || (max_pages > 0 && !page_table))
@@ -175,6 +177,8 @@ int csa_attention_decode(csa_attention* a, const uint16_t* q, const csa_cache* c
   c.paged = true;
   c.B = B;
   c.N = 1;
+  if (csa::attention_units(a, c) > 0x7fffffffLL)
+    return fail(CSA_ERR_ARG, "%s: too many tiles of 64 rows (items of 64 queries times rows / 64): 2^31 or more", what);
   CSA_CUDA(csa::launch_attention(a, c, (cudaStream_t)stream), "attention launch");
   return CSA_OK;
 }

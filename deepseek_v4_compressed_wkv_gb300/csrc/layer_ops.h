@@ -21,6 +21,7 @@ struct AttnCall {
   int B, N, start, kv_rows;
 };
 
+long long attention_units(const csa_attention* a, const AttnCall& call);  // above 2^31 - 1: too large a call
 cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_t s);
 size_t attention_workspace_bytes(int head_dim);
 

@@ -383,7 +383,8 @@ int csa_attention_create(int heads, int head_dim, int window, int sinks, float s
  *       nearest end and raises flag bit 1, see csa_attention_status)
  *  out  [B][N][heads][head_dim] bf16 dev
  *  lse  [B][N][heads] f32 dev or NULL
- * q, kv and out must be 16-byte aligned.  Returns CSA_OK or a negative csa_status. */
+ * q, kv and out must be 16-byte aligned; B * N * heads < 2^31, start_pos + N < 2^30,
+ * B * kv_rows < 2^31 - 1.  Returns CSA_OK or a negative csa_status. */
 int csa_attention_prefill(csa_attention* a, const uint16_t* q, const uint16_t* kv, int B, int N, int start_pos,
                           int kv_rows, const int32_t* lens, uint16_t* out, float* lse, csa_stream_t stream);
 
@@ -397,7 +398,9 @@ int csa_attention_prefill(csa_attention* a, const uint16_t* q, const uint16_t* k
  * A sequence's entries are split over the GPU and joined.  A length that is negative or beyond the
  * page table is taken as the nearest end and raises flag bit 1; an entry on a page outside the
  * cache is not read, raises flag bit 2 and leaves that sequence's results undefined.
- * q, out and the cache's arrays must be 16-byte aligned.  Returns CSA_OK or a negative csa_status. */
+ * q, out and the cache's arrays must be 16-byte aligned; pages * page_size < 2^31 - 1,
+ * max_pages * page_size < 2^30, and B * ceil(heads / 64) * (visible rows / 64 + 2) < 2^31.
+ * Returns CSA_OK or a negative csa_status. */
 int csa_attention_decode(csa_attention* a, const uint16_t* q, const csa_cache* cache, const int32_t* page_table,
                          int max_pages, const int32_t* lens, int B, uint16_t* out, float* lse, csa_stream_t stream);
 
