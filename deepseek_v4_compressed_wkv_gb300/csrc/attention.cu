@@ -286,19 +286,22 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t scale2) {
 // ---- the kernel's warps: 0-7 softmax (TMEM lane quarter = warp % 4, 32 of the 64 queries each); 8-15 the
 // epilogue, which reads O^T while the softmax warps go on with the next item; then two that issue the
 // MMAs (scores run up to two tiles ahead of values, also into the next item, without one loop having to
-// look out for both), one that schedules and copies the queries, and the rows' warps in two groups that
-// take alternate tiles (one group's tile can be in flight while the other waits for its stage).
+// look out for both), one that schedules and copies the queries, and the rows' warps: for latents two
+// groups that take alternate tiles (one group's can be in flight while the other waits for its stage).
 // One CTA an SM at every D: two of half the warps shared an SM up to D = 192 (their softmax warps
 // reading their own O^T) and took 118 us where this takes 66 (2 x 1777 tokens, D 128, window 512).
-// Codes need more warps to expand them (four a tile; with two, 16 expanding instructions a code pair and
-// warp took twice the time of the tile's MMAs) and give up half of the epilogue's.
+// Codes need more warps to expand them, which are half of the epilogue's, and all eight take a tile's
+// rows together, eight rows each: expanding them takes 1900 cycles of a tile's 3750 (alternate tiles by
+// four warps each: 52.3 us where this takes 49.0, 128 sequences of up to 2048 entries; a second set of
+// registers for the next tile's codes: 50.1).
 constexpr int kEpiWarp = 8;
 constexpr int kAttnThreads = 32 * 23;
 template <bool kFp4>
 struct Roles {
   static constexpr int kEpiWarps = kFp4 ? 4 : 8;
   static constexpr int kMma = kEpiWarp + kEpiWarps, kVal = kMma + 1, kQ = kMma + 2, kRow = kMma + 3;
-  static constexpr int kRowWarps = kAttnThreads / 32 - kRow, kRowGroup = kRowWarps / 2;  // a group brings a tile
+  static constexpr int kRowWarps = kAttnThreads / 32 - kRow;
+  static constexpr int kRowGroup = kFp4 ? kRowWarps : kRowWarps / 2;                    // a group brings a tile
   static constexpr int kTileRows = kTile / kRowGroup;                                   // of which a warp these
 };
 
@@ -668,7 +671,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // of the swizzled rows once: rows r and r + 4 side by side for 16-byte units, eight rows for units
     // that expand to 64 bytes
     const int r8 = kFp4 ? lane & 7 : (lane >> 3) + 4 * ((lane >> 2) & 1), u0 = kFp4 ? lane >> 3 : lane & 3;
-    constexpr int kGroups = kTileRows / 8;
+    constexpr int kGroups = kTileRows / 8;  // (latents)
     // a cache's rows are read once by a call: they are not to drive pieces out of L2
     const uint64_t policy = P.c.paged ? l2_evict_first() : l2_evict_normal();
     uint32_t k = 0;
@@ -714,7 +717,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       bool known = false;  // (found when the tile was looked ahead to)
 #pragma unroll 1
       for (int t = g.t0; t < g.t1; ++t, ++k) {
-        if ((int)(k & 1) != grp) continue;
+        if (!kFp4 && (int)(k & 1) != grp) continue;
         const uint32_t st = k & (nst - 1);
 #ifdef CSA_DEBUG_BOUNDS
         if (P.test_stall && k == 0) break;  // test of the time-out path: the first tile never comes
@@ -731,16 +734,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const uint8_t* at = kFp4 ? P.c.cache.codes + (size_t)max(row, 0) * (D / 2) : base + (size_t)max(row, 0) * (2 * D);
           if (row >= 0)
             for (int x = 0; x < (kFp4 ? D / 2 : 2 * D); x += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + x));
+          if (kFp4 && row >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(P.c.cache.scales + (size_t)row * (D / 16)));
         };
         if constexpr (kFp4) {
           // codes, expanded into the bf16 operand: a lane takes 32 codes and two scales (half a chunk) of
-          // its row at a time; the next eight rows' are on their way while eight are expanded
+          // its row at a time; they are on their way while the stage's last products run
           const int upr = D / 32;
           uint4 code[4];
           uint32_t sc[4];
-          auto load = [&](int i) {
-            const int r = kTileRows * w + 8 * i + r8, a = __shfl_sync(0xffffffffu, e0, r & 31),
-                      b = __shfl_sync(0xffffffffu, e1, r & 31), rr = r < 32 ? a : b;
+          const uint32_t r = kTileRows * w + r8;
+          {
+            const int a = __shfl_sync(0xffffffffu, e0, r & 31), b = __shfl_sync(0xffffffffu, e1, r & 31), rr = r < 32 ? a : b;
             const uint4* cp = reinterpret_cast<const uint4*>(P.c.cache.codes + (size_t)max(rr, 0) * (D / 2)) + u0;
             const uint16_t* sp = reinterpret_cast<const uint16_t*>(P.c.cache.scales + (size_t)max(rr, 0) * (D / 16)) + u0;
 #pragma unroll
@@ -749,38 +753,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               code[j] = live ? __ldg(cp + 4 * j) : make_uint4(0, 0, 0, 0);
               sc[j] = live ? __ldg(sp + 4 * j) : 0;
             }
-          };
-          load(0);
+          }
+          look_ahead(t + 1);
           if (!(ok = stage_free(st))) break;
-#pragma unroll 1
-          for (int i = 0; i < kGroups; ++i) {
-            uint4 cur[4];
-            uint32_t cs[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) cur[j] = code[j], cs[j] = sc[j];
-            if (i + 1 < kGroups) load(i + 1);
-            const uint32_t r = kTileRows * w + 8 * i + r8;
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t u = u0 + 4 * j;
+            if (4 * j >= upr) break;
+            if ((int)u >= upr) continue;
+            const uint32_t at = dst + (u >> 1) * kChunkBytes + r * 128;
+            const uint32_t word[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
+            const float s0 = e4m3_value(sc[j] & 255u), s1 = e4m3_value(sc[j] >> 8);
+            const uint32_t s2[2] = {bf16x2(s0, s0), bf16x2(s1, s1)};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t u = u0 + 4 * j;
-              if (4 * j >= upr) break;
-              if ((int)u >= upr) continue;
-              const uint32_t at = dst + (u >> 1) * kChunkBytes + r * 128;
-              const uint32_t word[4] = {cur[j].x, cur[j].y, cur[j].z, cur[j].w};
-              const float s0 = e4m3_value(cs[j] & 255u), s1 = e4m3_value(cs[j] >> 8);
-              const uint32_t s2[2] = {bf16x2(s0, s0), bf16x2(s1, s1)};
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const uint4 d = dequant8(word[q], s2[q >> 1]);
-                const uint32_t c = ((u & 1) * 4 + q) ^ (r & 7);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + c * 16), "r"(d.x), "r"(d.y), "r"(d.z),
-                             "r"(d.w)
-                             : "memory");
-              }
+            for (int q = 0; q < 4; ++q) {
+              const uint4 d = dequant8(word[q], s2[q >> 1]);
+              const uint32_t c = ((u & 1) * 4 + q) ^ (r & 7);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + c * 16), "r"(d.x), "r"(d.y), "r"(d.z),
+                           "r"(d.w)
+                           : "memory");
             }
           }
           hand_over(st);
-          look_ahead(t + 2);
         } else {
           const int e = __shfl_sync(0xffffffffu, e0, 0);
           const bool run = __all_sync(0xffffffffu, e0 >= 0 && e0 == e + lane && e1 == e + 32 + lane) != 0;
