@@ -17,6 +17,7 @@
 // long as it is near.  It begins as 0, and is only renewed (as the tile's maximum, with O^T and l
 // scaled) when a score passes it by 16 base-2 steps, or when a query's first scores are all below
 // -64: taking the maximum over rows costs an exchange between the warps that most tiles need not pay.
+// (Items of a single tile always pay it: with few rows the largest weight should be 1, which is exact.)
 //
 // What bounds it (probes on GB300, cycles): a 64 x 64 x 16 MMA takes 32 and a 128 x 64 x 16 one 48
 // (shared-memory reads of both operands at 128 bytes a cycle), so a tile of 64 rows at D = 512 costs
@@ -920,7 +921,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(raw[i]);
         const int v0 = t * kTile, v1 = min(v0 + kTile, g.s.cnt), v = v0 + 16 * qt + (lane >> 2);
-        bool renew = !ok;
+        bool renew = !ok || g.tiles == 1;
         uint32_t spoilt = 0;  // bits 0, 1: this thread's rows hold a NaN or infinity that a token must not see
         if (several) {
           // rows that only some of the item's tokens see
@@ -1035,7 +1036,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               const int v = begin < P.sinks ? begin : max(begin, P.window ? tt - P.window + 1 - g.s.jump : 0);
               before = v < v0 && (v < P.sinks ? v : v + g.s.jump) <= tt;
             }
-            const float m0 = red[threadIdx.x], m1 = y * sl - m0 > kStep || (!before && y > kFloor && y * sl < kLow) ? y * sl : m0;
+            const float m0 = red[threadIdx.x], m1 = y * sl - m0 > kStep || (!before && y > kFloor && (y * sl < kLow || g.tiles == 1)) ? y * sl : m0;
             red[threadIdx.x] = m1;
             red[64 + threadIdx.x] = before ? ex2(m0 - m1) : 1.0f;
           }

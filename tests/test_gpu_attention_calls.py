@@ -130,6 +130,18 @@ def test_queries_that_are_not_numbers_stay_in_their_rows():
     assert not torch.isfinite(out[~same]).any()
 
 
+@pytest.mark.parametrize("kind", ["latent", "fp4"])
+def test_a_single_visible_row_is_the_result(kind):
+    """Its weight is 1: the output is the row, without a rounding (an fp4 row's values are bf16 numbers)."""
+    a, P, q, (out, lse) = run_decode(64, 512, 16, [1, 1, 0, 1], kind, seed=21)
+    for b in (0, 1, 3):
+        assert torch.equal(out[b].double(), P.values[b][:1].expand(64, -1))
+    a, q, kv, (out, lse) = run_prefill(2, 50, 16, 128, 1, 0)
+    assert torch.equal(out, kv[:, :50, None].expand(-1, -1, 16, -1))
+    a, q, kv, (out, lse) = run_prefill(2, 60, 64, 256, 0, 0)
+    assert torch.equal(out[:, 0], kv[:, :1].expand(-1, 64, -1))
+
+
 def test_calls_that_are_too_large_are_refused():
     """Sizes that the kernels' 31-bit numbers do not hold; the addresses are never read."""
     lib, A = csa.load_library(), 4096
