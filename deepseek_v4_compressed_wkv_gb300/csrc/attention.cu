@@ -419,9 +419,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     constexpr int kTwo = kEpiWarps / 4;
     const int w = warp & 3, half = tid >> 7;
     bool ok = wait(l_full, seg - 1);
-    ok = ok && wait(&pv_done[kl & 1], kl >> 1);
     if (group_or<kEpiWarps>(2, !ok)) return false;
-    tc_fence_after();
     const bool whole = g.t0 == 0 && g.t1 == g.tiles;
     // a piece: slot 0 of the CTA for its first segment's, 1 for its last's (an item's first piece)
     const int slot = 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0);
@@ -442,7 +440,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         P.part_ml[slot * kCols + tid] = make_float2(l == 0.0f ? kFloor : m, l);  // (no row: no reference either)
       }
     }
-    group_sync<kEpiWarps>(2);
+    // (the sums are there before the last product over rows is done)
+    ok = wait(&pv_done[kl & 1], kl >> 1);
+    if (group_or<kEpiWarps>(2, !ok)) return false;
+    tc_fence_after();
     if (lane == 0) mbar_arrive(l_empty);
     auto give_back = [&](int block) {
       tc_fence_before();
@@ -455,6 +456,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // steps of 32 queries x 32 features (16 of a last block of 64) a warp; the next step's loads run
       // ahead of a step's stores
       const int steps = (chunks + 1) & ~1;  // two of a block
+      float2 f[4];
+      auto factors = [&](int c) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) f[q] = *reinterpret_cast<const float2*>(inv + 32 * c + 8 * q + 2 * (lane & 3));
+      };
+      if (kTwo == 2) factors(half);
       uint32_t o[2][16];
       tmem_ld_half(base + 32 * half, o[0]);
       tmem_ld_half(base + 32 * half + (16u << 16), o[1]);
@@ -462,9 +469,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int step = half; step < steps; step += kTwo) {
         const int x = step & ~1, c = step & 1;
         const bool full = x + 1 < chunks;
-        float2 f[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) f[q] = *reinterpret_cast<const float2*>(inv + 32 * c + 8 * q + 2 * (lane & 3));
+        if (kTwo == 1) factors(c);
         tmem_ld_wait();
         uint32_t v[2][2][4];
 #pragma unroll
