@@ -462,6 +462,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int q = 0; q < 4; ++q) f[q] = *reinterpret_cast<const float2*>(inv + 32 * c + 8 * q + 2 * (lane & 3));
       };
       if (kTwo == 2) factors(half);
+      // to [query][32 features] by transposed stores, 16 queries at a time; 16-byte units swizzled against
+      // conflicts: row r of 64 bytes, unit u at u ^ (r / 2 % 4)
+      uint8_t* const stage = sO + (warp & 7) * kStageOut;
+      const int r = 8 * (lane >> 4) + (lane & 7);
+      const uint32_t put = smem_addr(stage) + r * 64 + ((((lane >> 3) & 1) ^ ((r >> 1) & 3)) << 4);
+      const uint8_t* const get = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+      uint8_t* const to = reinterpret_cast<uint8_t*>(
+          P.c.out + (orow + (kTwo == 2 ? 32 * half : 0) + (lane >> 2)) * D + 32 * w + 8 * (lane & 3));
       uint32_t o[2][16];
       tmem_ld_half(base + 32 * half, o[0]);
       tmem_ld_half(base + 32 * half + (16u << 16), o[1]);
@@ -488,30 +496,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tmem_ld_half(at, o[0]);
           tmem_ld_half(at + (16u << 16), o[1]);
         }
-        // to [query][32 features] by transposed stores, 16 queries at a time; 16-byte units swizzled
-        // against conflicts
-        uint8_t* stage = sO + (warp & 7) * kStageOut;
-        const int r = 8 * (lane >> 4) + (lane & 7), u = lane & 3;
-        uint16_t* dst = P.c.out + (orow + 32 * c + (lane >> 2)) * D + x * 64 + w * (full ? 32 : 16) + 8 * u;
+        uint8_t* dst = to + (long long)(x * 128 + (full ? 0 : -32 * w)) + (kTwo == 1 ? 64 * D * c : 0);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            stmatrix4<true>(smem_addr(stage) + r * 64 + (((2 * h + ((lane >> 3) & 1)) ^ ((r >> 1) & 3)) << 4), v[i][h][0],
-                            v[i][h][1], v[i][h][2], v[i][h][3]);
+            stmatrix4<true>(put ^ (h << 5), v[i][h][0], v[i][h][1], v[i][h][2], v[i][h][3]);
           __syncwarp();
           uint4 y[2];
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const int rr = (lane >> 2) + 8 * z;
-            y[z] = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((u ^ ((rr >> 1) & 3)) << 4));
-          }
+          for (int z = 0; z < 2; ++z) y[z] = *reinterpret_cast<const uint4*>(get + 512 * z);
           __syncwarp();
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
             const int q = 32 * c + 16 * i + 8 * z + (lane >> 2);
-            if ((full || u < 2) && q < g.s.cols && in_bounds(orow + q, rows, P.flag))
-              *reinterpret_cast<uint4*>(dst + (size_t)(16 * i + 8 * z) * D) = y[z];
+            if ((full || (lane & 3) < 2) && q < g.s.cols && in_bounds(orow + q, rows, P.flag))
+              *reinterpret_cast<uint4*>(dst + (16 * i + 8 * z) * 2 * D) = y[z];
           }
         }
       }
