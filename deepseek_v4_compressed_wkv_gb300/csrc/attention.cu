@@ -1368,26 +1368,12 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  // Both kernels may be set up while the launch before them ends: what they read and write waits for it.
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kAttnThreads);
-  cfg.dynamicSmemBytes = sh.smem;
   a->launches += 1;
-  e = fp4 ? cudaLaunchKernelEx(&cfg, attention_kernel<true>, mq, mc, P) : cudaLaunchKernelEx(&cfg, attention_kernel<false>, mq, mc, P);
+  e = launch_early(fp4 ? attention_kernel<true> : attention_kernel<false>, dim3(grid), dim3(kAttnThreads), sh.smem, s, mq, mc, P);
   if (e != cudaSuccess || !P.split) return e;
-  cfg.dynamicSmemBytes = 0;
-  cfg.gridDim = P.few ? dim3(P.items, a->D / 4) : dim3(grid, a->D / 64);
-  cfg.blockDim = P.few ? dim3(64, 16) : dim3(256, 1);
   a->launches += 1;
-  return P.few ? cudaLaunchKernelEx(&cfg, attention_join_kernel<64, 16, 1>, P)
-             : cudaLaunchKernelEx(&cfg, attention_join_kernel<256, 1, 4>, P);
+  return P.few ? launch_early(attention_join_kernel<64, 16, 1>, dim3(P.items, a->D / 4), dim3(64, 16), 0, s, P)
+               : launch_early(attention_join_kernel<256, 1, 4>, dim3(grid, a->D / 64), dim3(256, 1), 0, s, P);
 }
 
 }  // namespace csa

@@ -1,15 +1,21 @@
 // The paged cache's write and the residual RMSNorm with an 8-bit output.
 #include "layer_ops.h"
+#include "tc_common.cuh"
 
 namespace csa {
 namespace {
+
+using namespace tcx;
 
 // ---------------------------------------------------------------------------------------
 // Cache write: entry e = b * G + i of the call's rows to index first[b] + i of sequence b.
 //
 // Bytes are moved once; one warp per entry, each array's row as units of the widest type its
-// addresses allow (a 512-wide latent is two 16-byte units a lane).  Bound by HBM (read + write)
-// for a prefill's entries, by the launch for a decode step's.
+// addresses allow (a 512-wide latent is two 16-byte units a lane).  8 x 2048 latents of 512 features
+// (33.6 MB) take 8 us in a stream, which is also what a call costs its host; a decode step's 128
+// entries are bound by the launch.  Entries and indices fit 32 bits: with 64-bit quotients the kernel
+// ran twice as many instructions (10.2 us with them and without the early start).  Asking for the
+// latent before its slot is looked up measured the same.
 
 struct AppendParams {
   csa_cache cache;
@@ -25,6 +31,7 @@ struct AppendParams {
 
 template <class T>
 __device__ __forceinline__ void copy_units(uint8_t* dst, const uint8_t* src, int bytes, int lane) {
+#pragma unroll 4
   for (int i = lane; i < bytes / (int)sizeof(T); i += 32)
     reinterpret_cast<T*>(dst)[i] = __ldg(reinterpret_cast<const T*>(src) + i);
 }
@@ -45,13 +52,16 @@ __device__ __forceinline__ void copy_row(uint8_t* dst, const uint8_t* src, int b
 constexpr int kAppendWarps = 8;
 
 __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const AppendParams P) {
+  griddep_wait();
+  griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const long long e = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
-  if (e >= (long long)P.B * P.G) return;
-  const int b = (int)(e / P.G), i = (int)(e % P.G);
+  const uint32_t e = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);  // (B * G is below 2^31)
+  if (e >= (uint32_t)P.B * (uint32_t)P.G) return;
+  const uint32_t b = e / (uint32_t)P.G, i = e - b * (uint32_t)P.G;
   if (P.mask && !P.mask[b]) return;
-  const long long j = (long long)P.first[b] + i, page = j / P.cache.page_size;
-  int bad = j < 0 ? 1 : page >= P.max_pages ? 2 : 0;
+  const long long index = (long long)P.first[b] + i;  // below 2^32
+  const uint32_t j = (uint32_t)index, size = (uint32_t)P.cache.page_size, page = j / size;
+  int bad = index < 0 ? 1 : page >= (uint32_t)P.max_pages ? 2 : 0;
   int p = 0;
   if (!bad) {
     p = P.page_table[(long long)b * P.max_pages + page];
@@ -61,13 +71,13 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const A
     if (P.status && lane == 0) atomicOr(P.status, bad);
     return;
   }
-  const long long row = (long long)p * P.cache.page_size + j % P.cache.page_size;
+  const long long row = (long long)p * size + (j - page * size);
   if (P.cache.latent)
-    copy_row((uint8_t*)P.cache.latent + row * P.lat_bytes, (const uint8_t*)P.in.latent + e * P.lat_bytes, P.lat_bytes,
+    copy_row((uint8_t*)P.cache.latent + row * P.lat_bytes, (const uint8_t*)P.in.latent + (size_t)e * P.lat_bytes, P.lat_bytes,
              P.lat_unit, lane);
   if (P.cache.codes) {
-    copy_row(P.cache.codes + row * P.code_bytes, P.in.codes + e * P.code_bytes, P.code_bytes, P.code_unit, lane);
-    copy_row(P.cache.scales + row * P.scale_bytes, P.in.scales + e * P.scale_bytes, P.scale_bytes, P.scale_unit, lane);
+    copy_row(P.cache.codes + row * P.code_bytes, P.in.codes + (size_t)e * P.code_bytes, P.code_bytes, P.code_unit, lane);
+    copy_row(P.cache.scales + row * P.scale_bytes, P.in.scales + (size_t)e * P.scale_bytes, P.scale_bytes, P.scale_unit, lane);
   }
 }
 
@@ -86,7 +96,7 @@ int common_unit(const void* a, const void* b, int bytes) {
 // the products with a scale's reciprocal are f32.
 //
 // 9 bytes a feature move through HBM, which bounds it: 16461 rows of 4096 with scales per 128 take
-// 97 us (607 MB, 6.3 TB/s).  Every load of a thread is asked for before the first value is used:
+// 95 us (607 MB, 6.4 TB/s, 95 % of a copy's).  Every load of a thread is asked for before the first value is used:
 // with each piece's residual stored before the next piece's loads, and eight divisions a piece, the
 // same rows took 112 us.  Two pieces a thread: one (512 threads, two CTAs' worth of them waiting at
 // each reduction) takes 134 us, four (a third of the warps) 114 us.  Few rows are bound by the launch.
@@ -141,6 +151,8 @@ __device__ __forceinline__ uint4 load16(const void* p) {
 // BLOCK: features per scale (32, 128, 0 for the row).  PIECES: 8-feature pieces a thread.
 template <int BLOCK, int PIECES>
 __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(const NormParams P) {
+  griddep_wait();
+  griddep_launch_dependents();
   __shared__ float red[2][32];
   const int T = blockDim.x, t = threadIdx.x, lane = t & 31, warp = threadIdx.y * (T >> 5) + (t >> 5);
   const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
@@ -264,11 +276,7 @@ cudaError_t launch_norm(const NormParams& P, cudaStream_t s) {
   const int T = (units + 32 * pieces - 1) / (32 * pieces) * 32;
   const int R = T >= 256 ? 1 : min(8, 256 / T);  // rows of a CTA
   const dim3 block(T, R), grid((unsigned)((P.rows + R - 1) / R));
-  if (pieces == 1)
-    rmsnorm_q8_kernel<BLOCK, 1><<<grid, block, 0, s>>>(P);
-  else
-    rmsnorm_q8_kernel<BLOCK, 2><<<grid, block, 0, s>>>(P);
-  return cudaGetLastError();
+  return launch_early(pieces == 1 ? rmsnorm_q8_kernel<BLOCK, 1> : rmsnorm_q8_kernel<BLOCK, 2>, grid, block, 0, s, P);
 }
 
 }  // namespace
@@ -292,8 +300,7 @@ cudaError_t launch_cache_append(const csa_cache& cache, const csa_out& in, int B
   P.code_unit = common_unit(cache.codes, in.codes, P.code_bytes);
   P.scale_unit = common_unit(cache.scales, in.scales, P.scale_bytes);
   const long long n = (long long)B * G;
-  cache_append_kernel<<<(unsigned)((n + kAppendWarps - 1) / kAppendWarps), kAppendWarps * 32, 0, s>>>(P);
-  return cudaGetLastError();
+  return launch_early(cache_append_kernel, dim3((unsigned)((n + kAppendWarps - 1) / kAppendWarps)), dim3(kAppendWarps * 32), 0, s, P);
 }
 
 cudaError_t launch_rmsnorm_residual_q8(const uint16_t* x, const uint16_t* residual, const float* gain, long long rows,

@@ -1,6 +1,8 @@
 // Launchers of the operators around the compressor (host side, enqueue only).
 #pragma once
 
+#include <type_traits>
+
 #include "csa_internal.cuh"
 
 namespace csa {
@@ -24,6 +26,24 @@ struct AttnCall {
 long long attention_units(const csa_attention* a, const AttnCall& call);  // above 2^31 - 1: too large a call
 cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_t s);
 size_t attention_workspace_bytes(int head_dim);
+
+// Launches a kernel that may be set up while the launch before it in the stream ends (it waits for that
+// one, griddep_wait, before it touches memory): 2 of the 10 us that a small kernel takes in a stream.
+template <class... Params>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                         const std::remove_cv_t<Params>&... params) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, params...);
+}
 
 cudaError_t launch_cache_append(const csa_cache& cache, const csa_out& in, int B, int G, const int32_t* page_table,
                                 int max_pages, const int32_t* first, const uint8_t* mask, int* status, cudaStream_t s);

@@ -210,6 +210,24 @@ def test_append_leaves_out_what_does_not_fit():
     assert torch.equal(c.latent[1, 3], e["latent"][0, 0])
 
 
+def test_append_beyond_32_bit_offsets():
+    """More than 2^32 bytes of entries in one call, to pages in reverse order, an index that the page size
+    does not divide first; and an index near 2^31 into a table that ends long before."""
+    G, page, D = 2 ** 22 + 77, 48, 512
+    n = -(-(G + 5) // page)
+    new = torch.empty(1, G, D, dtype=torch.bfloat16, device=DEV)
+    new.view(torch.int16)[0] = torch.arange(G, device=DEV, dtype=torch.int32).to(torch.int16)[:, None]
+    pool = torch.zeros(n, page, D, dtype=torch.bfloat16, device=DEV)
+    table = torch.arange(n - 1, -1, -1, dtype=torch.int32, device=DEV)[None]
+    cache = csa.PagedCache(pool)
+    cache.append({"latent": new}, table, torch.tensor([5], dtype=torch.int32, device=DEV))
+    got = pool.flip(0).view(-1, D).view(torch.int16)
+    assert torch.equal(got[5:5 + G], new[0].view(torch.int16)) and not got[:5].any() and not got[5 + G:].any()
+    before = got.sum(dtype=torch.int64)
+    cache.append({"latent": new[:, :100].contiguous()}, table, torch.tensor([2 ** 31 - 50], dtype=torch.int32, device=DEV))
+    assert pool.view(torch.int16).sum(dtype=torch.int64) == before
+
+
 def test_append_refusals():
     c = csa.PagedCache.allocate(3, 4, 64)
     e, t, f = entries(2, 2, 64, 0, 9), torch.zeros(2, 2, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
@@ -323,3 +341,46 @@ def test_a_decode_step_in_a_graph():
         want = step(twin, caches[1])
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), i
+
+
+def test_a_run_without_pauses_gives_what_it_gives_with_pauses():
+    """Norm, cache write and attention in a row, each set up while the one before ends, over buffers that
+    the next step overwrites: 40 steps enqueued at once against the same steps with a pause after each call."""
+    B, H, D, page, n = 12, 64, 512, 16, 300
+    g = gen(31)
+    start = torch.randn(B * 20, page, D, generator=g, device=DEV).bfloat16()
+    table = torch.randperm(B * 20, generator=g, device=DEV).to(torch.int32).view(B, 20)
+    xs = [torch.randn(B, D, generator=g, device=DEV).bfloat16() for _ in range(40)]
+    gain = 1 + 0.1 * torch.randn(D, generator=g, device=DEV)
+    runs = []
+    for pause in (True, False):
+        cache, a = csa.PagedCache(start.clone()), csa.Attention(H, D, 200, 4)
+        x, res, pos = torch.empty_like(xs[0]), torch.zeros_like(xs[0]), torch.arange(B, dtype=torch.int32, device=DEV) + n - 60
+        kept = []
+
+        def wait():
+            if pause:
+                torch.cuda.synchronize()
+
+        for i in range(40):
+            x.copy_(xs[i])
+            wait()
+            o = csa.rmsnorm_residual_q8(x, res, gain, inplace=True)
+            wait()
+            cache.append({"latent": o["y"]}, table, pos)
+            wait()
+            pos += 1
+            q = o["y"][:, None].expand(B, H, D) * 1
+            x.fill_(math.nan)
+            out, lse = a.decode(q, cache, table, pos)
+            wait()
+            o["y"].fill_(math.nan)
+            kept.append((out, lse, o["q"].view(torch.uint8), res.clone()))
+            q.fill_(math.nan)
+        torch.cuda.synchronize()
+        cache.status()
+        assert a.device_status() == 0
+        runs.append((kept, cache.latent.clone()))
+    for p, q in zip(runs[0][0], runs[1][0]):
+        assert all(torch.equal(x, y) for x, y in zip(p, q))
+    assert torch.isfinite(runs[0][0][-1][0]).all() and torch.equal(runs[0][1], runs[1][1])
