@@ -21,16 +21,33 @@
 //
 // What bounds it (probes on GB300, cycles): a 64 x 64 x 16 MMA takes 32 and a 128 x 64 x 16 one 48
 // (shared-memory reads of both operands at 128 bytes a cycle), so a tile of 64 rows at D = 512 costs
-// 1024 + 768; its 64 KB arrive from HBM in 2510 (26 bytes a cycle and SM, 7.2 TB/s).  Decode over
-// latents is therefore bound by HBM, over codes (18 KB a tile) by the MMAs' operand reads.  Rows
-// come by 16-byte cp.async, which takes any page size and leaves hidden rows out (zeros) at the rate
-// of tiled TMA boxes (760 cycles a tile from L2, against 8010 for four-row TMA gathers).
+// 1024 + 768; its 64 KB arrive from HBM in 2510 (26 bytes a cycle and SM, 7.2 TB/s) and from L2 in 700.
+// A tile passes four stations one after the other, its copy, the scores (1100), the softmax (1200)
+// and the values (900), and shared memory holds two tiles of 512 features beside the queries, so two
+// tiles go through them at a time:
+//   decode over latents  3200 cycles a tile, 0.87 of HBM's rate while tiles stream; 128 sequences of up
+//                        to 2048 entries, 64 heads of 512: 47.6 us in all (152 MB, 3.2 TB/s), of which 4
+//                        pass before the first copy (lengths, shares, page table: one after the other),
+//                        2.3 until it lands, 2.5 in the last pieces' stores and 8.5 in their join
+//   decode over codes    3750 cycles a tile, 1900 of them the expansion of codes to bf16: 49.0 us
+//   a prompt's window    7400 cycles an item of two tiles: the epilogue reads O^T for 5000 of them, which
+//                        the next item's values wait for block by block (there is no room for a second
+//                        O^T at D = 512): 4096 tokens, 64 heads of 512, window 128: 112.6 us (542 MB, 4.8 TB/s)
+//   narrow heads         1250 cycles a tile at D = 128, the softmax alone: 2 x 1777 tokens, 16 heads, window
+//                        512: 45.2 us
 //
-// Work is cut by tiles: the call's tiles (and one's time for each item), in item order, are divided evenly over the CTAs, so ragged
-// lengths and few long sequences fill the GPU alike; an item cut by a CTA boundary leaves partial
-// (m, l, O) pieces in the workspace, which a second kernel joins.  Where no item is longer than
-// kJoinTiles tiles the boundaries are moved to item starts instead: the imbalance costs less than
-// pieces and their join.
+// Measured and not taken: stages handed over by blocks of 128 features (decode 128 x 2048 1 % faster, a
+// windowed prompt 2 to 8 % and codes 4 % slower); products over rows in steps that leave out a last
+// tile's absent rows (1 % slower, 2 % faster for windows of 128 + 4); rows by four-row TMA gathers (8010
+// cycles a tile; cp.async 760 from L2, any page size, absent rows as zeros); a second set of registers in
+// the epilogue (spills: 112 -> 146 us).
+//
+// Work is cut by tiles: the call's tiles, in item order (and a tile's time for each item), are divided
+// evenly over the CTAs, so ragged lengths and few long sequences fill the GPU alike; an item cut by a CTA
+// boundary leaves partial (m, l, O) pieces in the workspace, which a second kernel joins.  Where no
+// item is longer than kJoinTiles tiles the boundaries are moved to item starts instead: the imbalance
+// costs less than pieces and their join.  Without a tile's time for each item, CTAs with three items
+// ended 4 us after those with one (decode 128 x 2048: 49.3 -> 47.6 us).
 #include <atomic>
 #include <cstdlib>
 

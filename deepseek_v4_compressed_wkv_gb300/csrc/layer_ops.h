@@ -29,6 +29,9 @@ size_t attention_workspace_bytes(int head_dim);
 
 // Launches a kernel that may be set up while the launch before it in the stream ends (it waits for that
 // one, griddep_wait, before it touches memory): 2 of the 10 us that a small kernel takes in a stream.
+// Such a kernel lets its own successor be set up only behind its wait, so that a kernel that has
+// started finds everything before its direct predecessor complete (the compressor's decode reads its
+// weights, and then its state, before it waits).
 template <class... Params>
 cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                          const std::remove_cv_t<Params>&... params) {
