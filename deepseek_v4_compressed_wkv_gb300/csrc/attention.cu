@@ -44,10 +44,10 @@
 //
 // Work is cut by tiles: the call's tiles, in item order (and a tile's time for each item), are divided
 // evenly over the CTAs, so ragged lengths and few long sequences fill the GPU alike; an item cut by a CTA
-// boundary leaves partial (m, l, O) pieces in the workspace, which a second kernel joins.  Where no
-// item is longer than kJoinTiles tiles the boundaries are moved to item starts instead: the imbalance
-// costs less than pieces and their join.  Without a tile's time for each item, CTAs with three items
-// ended 4 us after those with one (decode 128 x 2048: 49.3 -> 47.6 us).
+// boundary leaves partial (m, l, O) pieces in the workspace, which a second kernel joins.  Where cutting
+// would cost more than it saves, items are whole: one a CTA, or a share's by their starts.  Without a
+// tile's time for each item, CTAs with three items ended 4 us after those with one (decode 128 x 2048:
+// 49.3 -> 47.6 us).
 #include <atomic>
 #include <cstdlib>
 
@@ -64,8 +64,8 @@ constexpr int kCols = 64;                      // queries of an item
 constexpr int kChunkBytes = 8192;              // 64 rows x 64 features bf16: one column of swizzled atoms
 constexpr int kPBytes = kTile * kCols * 2;     // one weights buffer
 constexpr int kStageOut = 1024;                // a warp's staging of 16 queries x 32 features bf16
-constexpr int kJoinTiles = 6;   // items longer than this are split
-constexpr int kMinTiles = 4;    // a split call gives a CTA at least this many tiles
+constexpr int kCutMany = 8;  // units (see units_of) that cutting items costs: their pieces and the join
+constexpr int kCutFew = 3;   // and where the items are few
 constexpr float kStep = 16.0f;  // base-2 steps a score may pass the reference by
 constexpr float kLow = -64.0f;  // where the first scores are all lower, 0 is no reference for them
 constexpr float kFloor = -1e38f;  // the maximum of no scores
@@ -579,8 +579,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       const int total = __shfl_sync(0xffffffffu, pre, 31);
       pre -= sum;
-      const bool cut = top > kJoinTiles;
-      const int ctas = cut ? min((int)gridDim.x, max(1, total / kMinTiles)) : (int)gridDim.x;
+      // Items are cut where that saves more units than it costs.  Uncut, each has a CTA of its own or, where
+      // they are more than the CTAs, a CTA has its rounds of equal items or at most one more than its share.
+      // (64 heads of 512: 128 x 512 entries 22.8 us uncut and 33.8 us cut, 300 x 512 40.6 and 54; 128 sequences
+      // of up to 1024 34.6 us cut and 48 us uncut.  Shares are four units at least, but two up to 64 CTAs: the
+      // fewer pieces join faster, 1 x 32768 22.6 us against 24 us, the shorter shares matter where they are
+      // few, 1 x 4096 14.9 us against 17 us.)
+      int ctas = min((int)gridDim.x, max(1, max(min(64, total / 2), total / 4)));
+      const int longest = units_of(top);
+      const bool own = P.items <= (int)gridDim.x;
+      const long long uncut = own ? longest
+                              : total == (long long)P.items * longest
+                                  ? (long long)((P.items - 1) / (int)gridDim.x + 1) * longest
+                                  : (long long)total / (int)gridDim.x + longest;
+      const bool cut = uncut > total / ctas + (P.few ? kCutFew : kCutMany);
+      if (!cut) ctas = gridDim.x;
       // share i begins at each * i + min(i, more)
       const int each = total / ctas, more = total - each * ctas, i0 = min((int)blockIdx.x, ctas), i1 = min(i0 + 1, ctas);
       const int a = each * i0 + min(i0, more), e = each * i1 + min(i1, more);
@@ -607,6 +620,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       first_item = found[0][0], first_tile = found[0][1], first_index = found[0][2];
       share = found[1][2] - found[0][2];
+      if (own && !cut) {
+        first_item = blockIdx.x, first_tile = 0;
+        share = first_item < P.items ? units_of(tiles_of(seen_rows(P, first_item))) : 0;
+      }
       if (lane == 0) {
         work[0] = each, work[1] = more;  // (read by whoever leaves an item's first piece)
         if (!P.few) P.record[blockIdx.x] = make_int2(-1, 0);
@@ -1305,6 +1322,10 @@ size_t attention_workspace_bytes(int head_dim) {
   return 2 * (size_t)current_sm_count() * (kCols * (head_dim * sizeof(float) + sizeof(float2)) + sizeof(int2)) + 64;
 }
 
+// Few items have many pieces each, and a join of their own (1 x 32768 entries 22.6 us, 4 x 8192 28 us
+// against 36 us with the other; 9 x 2000 25 us against 35 us with this one).
+static bool few_items(long long items, int sms) { return items * 32 <= sms; }
+
 // The units (see units_of) that a call whose items may be cut can have at most; 0 where none is cut.
 long long attention_units(const csa_attention* a, const AttnCall& call) {
   // the longest range of rows that this call can have decides whether items may be cut
@@ -1312,8 +1333,10 @@ long long attention_units(const csa_attention* a, const AttnCall& call) {
   long long most = call.paged ? (long long)call.max_pages * call.cache.page_size : (long long)call.start + call.N;
   const long long window = (long long)a->window + a->sinks + (kCols - 1) / a->heads + 1;
   if (a->window && most > window) most = window;
-  // (a prompt with several items a CTA is not: drawing them, the longest first, balances as well)
-  if (most <= (long long)kJoinTiles * kTile || (!call.paged && items >= 4LL * a->sms)) return 0;
+  // (a share is two units at least: shorter items than these are never cut; nor is a prompt with several
+  // items a CTA, where drawing them, the longest first, balances as well: 700 tokens of 64 heads over
+  // their own rows take 57 us drawn and 81 us cut, 200 tokens behind 2000 others 111 us drawn and 88 us cut)
+  if (most <= ((few_items(items, a->sms) ? kCutFew : kCutMany) + 1) * (long long)kTile || (!call.paged && items >= 4LL * a->sms)) return 0;
   return items * ((most + kTile - 1) / kTile + 1);
 }
 
@@ -1360,7 +1383,7 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
   const long long shares = P.split ? units : P.items;
   const int grid = (int)(shares < a->sms ? shares : a->sms);
   P.ctas = grid;
-  P.few = P.items * 8LL <= grid;
+  P.few = few_items(P.items, a->sms);
   CUtensorMap mq;
   {
     cuuint64_t dims[2] = {(cuuint64_t)a->D, (cuuint64_t)call.B * call.N * a->heads};
