@@ -328,7 +328,7 @@ int csa_rope_table(const csa_options* opt, int pos0, int npos, float* cos_out, f
  *   out[t][h]   = sum_j exp(S[h][j] - lse[t][h]) c[j]
  *   no visible j: out = 0, lse = -inf
  *
- * Scores, softmax statistics and sums are f32; the weights exp(S - running maximum) are rounded to
+ * Scores, softmax statistics and sums are f32; the weights exp(S - m), m near the maximum, are rounded to
  * bf16 for the second product and out is rounded to bf16 once.  Rows that are not visible to a
  * query are not read for it: what they hold (NaN, infinities) cannot reach its result. */
 
