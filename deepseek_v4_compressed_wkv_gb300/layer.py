@@ -101,7 +101,8 @@ class PagedCache:
         self._struct = _Cache(*ptr, self.pages, self.page_size, D, fp4)
         self._ref = ctypes.addressof(self._struct)
         self._arrays = [t for t in (latent, codes, scales) if t is not None]
-        self._flag = None
+        # made here: an append on another stream, or in a captured graph, must not have to clear it
+        self._flag = torch.zeros(1, dtype=_I32, device=base.device)
         self._append = load_library().csa_cache_append
 
     @classmethod
@@ -116,7 +117,7 @@ class PagedCache:
     def append(self, entries: dict, page_table, first, mask=None, stream=None):
         """Writes entries (a compressor call's outputs, [B, G, ..], or [B, ..] for one each) of
         sequence b to indices first[b] .. of its pages, where mask[b] is not 0.  page_table int32
-        [B, max_pages], first int32 [B], mask u8 [B] or None."""
+        [B, max_pages], first int32 [B], mask u8 [B] or None.  No entries: nothing is done."""
         dev = _current_device()
         if self.device != dev:
             raise CSAError(f"the cache is on cuda:{self.device}, but the current CUDA device is cuda:{dev}")
@@ -133,8 +134,8 @@ class PagedCache:
             if t.shape[-1] != pool.shape[2] or t.shape[0] != B or t.numel() != B * G * pool.shape[2]:
                 raise CSAError(f"{name} must be [{B}, {G}, {pool.shape[2]}], got {tuple(t.shape)}")
             src[i] = _want(name, t, pool.dtype, t.shape, dev)
-        if self._flag is None:
-            self._flag = torch.zeros(1, dtype=_I32, device=f"cuda:{dev}")
+        if B == 0 or G == 0:  # (a prefill of fewer tokens than a group has emits nothing)
+            return
         pt = _want("page_table", page_table, _I32, (B, page_table.shape[-1]), dev)
         fi = _want("first", first, _I32, (B,), dev)
         mk = None if mask is None else _want("mask", mask, _U8, (B,), dev)
@@ -152,7 +153,7 @@ class PagedCache:
     def status(self):
         """Raises CSAError if an append since the last call left an entry out (a negative index, an
         index beyond the page table, or a page outside the cache)."""
-        bits = 0 if self._flag is None else int(self._flag.item())
+        bits = int(self._flag.item())
         if bits:
             self._flag.zero_()
             what = [w for b, w in ((1, "a negative index"), (2, "an index beyond the page table"),

@@ -383,7 +383,7 @@ int csa_attention_create(int heads, int head_dim, int window, int sinks, float s
  *       nearest end and raises flag bit 1, see csa_attention_status)
  *  out  [B][N][heads][head_dim] bf16 dev
  *  lse  [B][N][heads] f32 dev or NULL
- * q, kv and out must be 16-byte aligned; B * N * heads < 2^31, start_pos + N < 2^30,
+ * q, kv and out must be 16-byte aligned; B >= 1, N >= 1, B * N * heads < 2^31, start_pos + N < 2^30,
  * B * kv_rows < 2^31 - 1.  Returns CSA_OK or a negative csa_status. */
 int csa_attention_prefill(csa_attention* a, const uint16_t* q, const uint16_t* kv, int B, int N, int start_pos,
                           int kv_rows, const int32_t* lens, uint16_t* out, float* lse, csa_stream_t stream);

@@ -210,6 +210,26 @@ def test_append_leaves_out_what_does_not_fit():
     assert torch.equal(c.latent[1, 3], e["latent"][0, 0])
 
 
+def test_append_of_nothing():
+    """A prefill of fewer tokens than a group has no entries: appending them does nothing; a cache that an
+    append on another stream is the first to use reports what that left out."""
+    c = csa.PagedCache.allocate(3, 4, 64)
+    none, table = torch.zeros(2, 0, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(2, 1, dtype=torch.int32, device=DEV)
+    c.append({"latent": none}, table, torch.zeros(2, dtype=torch.int32, device=DEV))
+    c.append({"latent": none[:0]}, table[:0], torch.zeros(0, dtype=torch.int32, device=DEV))
+    with pytest.raises(csa.CSAError, match="must be"):
+        c.append({"latent": none[:1]}, table, torch.zeros(2, dtype=torch.int32, device=DEV))
+    c.status()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    one = torch.ones(1, 1, 64, dtype=torch.bfloat16, device=DEV)
+    c.append({"latent": one}, table[:1], torch.full((1,), 9, dtype=torch.int32, device=DEV), stream=s)
+    torch.cuda.synchronize()
+    with pytest.raises(csa.CSAError, match="beyond the page table"):
+        c.status()
+    assert not c.latent.any()
+
+
 def test_append_beyond_32_bit_offsets():
     """More than 2^32 bytes of entries in one call, to pages in reverse order, an index that the page size
     does not divide first; and an index near 2^31 into a table that ends long before."""
