@@ -40,7 +40,7 @@ class _Cache(ctypes.Structure):
 def _want(name, t, dtype, shape, device):
     """The data pointer of a contiguous CUDA tensor of the given type and shape on the current
     device (a pointer into another GPU's memory would fault)."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous() and t.get_device() == device:
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():  # (-1 on the CPU)
         return t.data_ptr()
     if t.dtype != dtype:
         raise CSAError(f"{name} must be {dtype}, got {t.dtype}")
@@ -261,7 +261,8 @@ def rmsnorm_residual_q8(x, residual, gain, eps: float = 1e-6, scale_block: int =
     Returns residual (the sum, bf16, written over the one passed in with inplace; x itself without a
     residual), y (bf16, None without y), q (float8_e4m3fn) and its scales: f32 [.., dim / 128] (scale_block 128), f32 [.., 1]
     (0: one per row) or float8_e8m0fnu [.., dim / 32] (32)."""
-    dim = x.shape[-1]
+    shape = x.shape
+    dim = shape[-1]
     if scale_block not in (0, 32, 128):
         raise CSAError(f"scale_block must be 0, 32 or 128, got {scale_block}")
     if dim == 0 or dim % (128 if scale_block == 128 else 32):
@@ -269,15 +270,18 @@ def rmsnorm_residual_q8(x, residual, gain, eps: float = 1e-6, scale_block: int =
     if inplace and residual is None:
         raise CSAError("inplace writes over a residual: none was given")
     dev = _current_device()
-    xp = _want("x", x, _BF16, x.shape, dev)
-    rp = None if residual is None else _want("residual", residual, _BF16, x.shape, dev)
+    xp = _want("x", x, _BF16, shape, dev)
+    rp = None if residual is None else _want("residual", residual, _BF16, shape, dev)
     gp = _want("gain", gain, _F32, (dim,), dev)
-    make, s = (None, _raw_stream(dev)) if stream is None else (_Here(stream, (x, residual, gain)), stream.cuda_stream)
-    empty, like = (_empty, _empty_like) if make is None else (functools.partial(make, _empty), functools.partial(make, _empty_like))
+    if stream is None:
+        empty, like, s = _empty, _empty_like, _raw_stream(dev)
+    else:
+        make, s = _Here(stream, (x, residual, gain)), stream.cuda_stream
+        empty, like = functools.partial(make, _empty), functools.partial(make, _empty_like)
     total = x if residual is None else residual if inplace else like(x)
     yt = like(x) if y else None
     q = like(x, dtype=_E4M3)
-    scales = empty((*x.shape[:-1], dim // (scale_block or dim)), dtype=_E8M0 if scale_block == 32 else _F32, device=x.device)
+    scales = empty(shape[:-1] + (dim // (scale_block or dim),), dtype=_E8M0 if scale_block == 32 else _F32, device=x.device)
     rc = load_library().csa_rmsnorm_residual_q8(xp, rp, gp, x.numel() // dim, dim, eps, scale_block,
                                                 None if residual is None else total.data_ptr(),
                                                 None if yt is None else yt.data_ptr(), q.data_ptr(), scales.data_ptr(), s)

@@ -328,9 +328,9 @@ int csa_rope_table(const csa_options* opt, int pos0, int npos, float* cos_out, f
  *   out[t][h]   = sum_j exp(S[h][j] - lse[t][h]) c[j]
  *   no visible j: out = 0, lse = -inf
  *
- * Scores, softmax statistics and sums are f32; the weights exp(S - m), m near the maximum, are rounded to
- * bf16 for the second product and out is rounded to bf16 once.  Rows that are not visible to a
- * query are not read for it: what they hold (NaN, infinities) cannot reach its result. */
+ * Scores, softmax statistics and sums are f32; the weights exp(S - m), m near the maximum, are
+ * rounded to bf16 for the second product and out is rounded to bf16 once.  Rows that are not
+ * visible to a query are not read for it: what they hold (NaN, infinities) cannot reach its result. */
 
 /* A paged cache of entries (dev arrays owned by the caller): page p, slot s is row
  * p * page_size + s of each array, in csa_out's element layouts.  latent holds the entries' bf16
