@@ -307,8 +307,8 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t scale2) {
 // MMAs (scores run up to two tiles ahead of values, also into the next item, without one loop having to
 // look out for both), one that schedules and copies the queries, and the rows' warps: for latents two
 // groups that take alternate tiles (one group's can be in flight while the other waits for its stage).
-// One CTA an SM at every D: two of half the warps shared an SM up to D = 192 (their softmax warps
-// reading their own O^T) and took 118 us where this takes 66 (2 x 1777 tokens, D 128, window 512).
+// One CTA an SM at every D: two of half the warps sharing an SM up to D = 192 (their softmax warps
+// reading their own O^T) took 118 us where one took 66 (2 x 1777 tokens, D 128, window 512).
 // Codes need more warps to expand them, which are half of the epilogue's, and all eight take a tile's
 // rows together, eight rows each: expanding them takes 1900 cycles of a tile's 3750 (alternate tiles by
 // four warps each: 52.3 us where this takes 49.0, 128 sequences of up to 2048 entries; a second set of
@@ -1179,7 +1179,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 //   M = max m_p;  out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p
 // A thread takes four values (two queries, features d and d + 8) of every kGroups-th piece, kReps times
 // 16 features on; the groups' results are merged like pieces, in order: nothing depends on timing.
-// Few items have many pieces each (16 groups, the item over D / 4 CTAs), many items a few.
+// Few items have many pieces each (16 groups, the item over D / 4 CTAs, read in one pass with a running
+// maximum: 1 x 32768 entries 22.4 us; maxima first, with spilled registers, 23.2, 4 x 8192 28.5 and 32.2),
+// many items a few (128 sequences of up to 2048 entries: 8.5 us for 36 MB of pieces, which lie in L2).
 template <int kLanes, int kGroups, int kReps>
 __global__ void __launch_bounds__(kLanes * kGroups, 1024 / (kLanes * kGroups)) attention_join_kernel(const __grid_constant__ AttnParams P) {
   __shared__ float4 acc[kGroups > 1 ? kGroups : 1][kLanes];
@@ -1239,19 +1241,30 @@ __global__ void __launch_bounds__(kLanes * kGroups, 1024 / (kLanes * kGroups)) a
     s = seen_rows(P, blockIdx.x);
     if (rec.x < 0 || s.cols == 0) return;
     auto slot = [&](int p) { return 2 * (rec.x + p) + (p == 0 ? 1 : 0); };
-#pragma unroll 4
-    for (int p = grp; p < rec.y; p += kGroups) {
-      const float4 z = stats(slot(p));
-      y.x = fmaxf(y.x, z.x), y.z = fmaxf(y.z, z.z);
-    }
     a[0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int p = grp; p < rec.y; p += kGroups) {
-      const float4 z = stats(slot(p)), o = quad(slot(p), 0);
-      const float f0 = ex2(z.x - y.x), f1 = ex2(z.z - y.z);
-      y.y = fmaf(z.y, f0, y.y), y.w = fmaf(z.w, f1, y.w);
-      a[0].x = fmaf(o.x, f0, a[0].x), a[0].y = fmaf(o.y, f1, a[0].y);
-      a[0].z = fmaf(o.z, f0, a[0].z), a[0].w = fmaf(o.w, f1, a[0].w);
+#pragma unroll 1
+    for (int p = grp; p < rec.y; p += 2 * kGroups) {  // two pieces at once; the sums are scaled as the maximum grows
+      float4 z[2], o[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int pp = p + i * kGroups;
+        const bool there = pp < rec.y;
+        z[i] = there ? stats(slot(pp)) : make_float4(kFloor, 0.0f, kFloor, 0.0f);
+        o[i] = there ? quad(slot(pp), 0) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      float2 top = make_float2(y.x, y.z);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) top.x = fmaxf(top.x, z[i].x), top.y = fmaxf(top.y, z[i].z);
+      const float k0 = ex2(y.x - top.x), k1 = ex2(y.z - top.y);
+      y = make_float4(top.x, y.y * k0, top.y, y.w * k1);
+      a[0] = make_float4(a[0].x * k0, a[0].y * k1, a[0].z * k0, a[0].w * k1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float f0 = ex2(z[i].x - top.x), f1 = ex2(z[i].z - top.y);
+        y.y = fmaf(z[i].y, f0, y.y), y.w = fmaf(z[i].w, f1, y.w);
+        a[0].x = fmaf(o[i].x, f0, a[0].x), a[0].y = fmaf(o[i].y, f1, a[0].y);
+        a[0].z = fmaf(o[i].z, f0, a[0].z), a[0].w = fmaf(o[i].w, f1, a[0].w);
+      }
     }
   }
   if constexpr (kGroups > 1) {
@@ -1259,9 +1272,11 @@ __global__ void __launch_bounds__(kLanes * kGroups, 1024 / (kLanes * kGroups)) a
     __syncthreads();
     if (grp == 0) {
       float2 top = make_float2(kFloor, kFloor);
+#pragma unroll 4
       for (int i = 0; i < kGroups; ++i)
         top.x = fmaxf(top.x, ml[i][threadIdx.x].x), top.y = fmaxf(top.y, ml[i][threadIdx.x].z);
       y = make_float4(top.x, 0.0f, top.y, 0.0f), a[0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
       for (int i = 0; i < kGroups; ++i) {
         const float4 z = ml[i][threadIdx.x], o = acc[i][threadIdx.x];
         const float f0 = ex2(z.x - top.x), f1 = ex2(z.z - top.y);
