@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int each = total / ctas, more = total - each * ctas, i0 = min((int)blockIdx.x, ctas), i1 = min(i0 + 1, ctas);
       const int a = each * i0 + min(i0, more), e = each * i1 + min(i1, more);
       // a boundary x: the item it falls in or, without cutting, the first item that starts from it on
-      int found[2][3] = {{P.items, 0, total}, {P.items, 0, total}};
+      // (scalars: an array of both would lie in local memory)
 #pragma unroll 1
       for (int w = 0; w < 2; ++w) {
         const int x = w ? e : a;
@@ -616,11 +616,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         const uint32_t who = __ballot_sync(0xffffffffu, x >= pre && x < pre + sum);
         const int from = who ? __ffs(who) - 1 : 0;
-        found[w][0] = __shfl_sync(0xffffffffu, item, from), found[w][1] = __shfl_sync(0xffffffffu, tile, from);
-        found[w][2] = __shfl_sync(0xffffffffu, start, from);
+        start = __shfl_sync(0xffffffffu, start, from);
+        if (w == 0) {
+          first_item = __shfl_sync(0xffffffffu, item, from), first_tile = __shfl_sync(0xffffffffu, tile, from);
+          first_index = start;
+        } else {
+          share = start - first_index;
+        }
       }
-      first_item = found[0][0], first_tile = found[0][1], first_index = found[0][2];
-      share = found[1][2] - found[0][2];
       if (own && !cut) {
         first_item = blockIdx.x, first_tile = 0;
         share = first_item < P.items ? units_of(tiles_of(seen_rows(P, first_item))) : 0;
