@@ -103,6 +103,7 @@ struct AttnParams {
 #ifdef CSA_DEBUG_BOUNDS
   uint64_t wait_ns;  // the time-out test shortens the waits
   int test_stall;    // and leaves out each CTA's first tile
+  int test_late;     // or publishes each CTA's first segment only once a wait for it has run out
 #endif
 };
 
@@ -416,12 +417,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-  // the next segment, for every role but the scheduling warp
+  // The next segment, for every role but the scheduling warp; false behind the last one and after an
+  // abort.  The softmax's and the epilogue's warps meet at named barriers, which have no time limit, and
+  // after an abort one of them may still find a slot written that another has given up on: they go on or
+  // leave by their group's common decision, all others by the warp's own.
   uint32_t seg = 0;  // segments read
   Segment g;
   auto next = [&]() {
     const uint32_t slot = seg % kRing;
-    if (!__all_sync(0xffffffffu, wait(&g_full[slot], seg / kRing))) return false;
+    const bool there = wait(&g_full[slot], seg / kRing);
+    if (warp < kEpiWarp ? group_or(1, !there) : warp < kMmaWarp ? group_or<kEpiWarps>(2, !there) : !__all_sync(0xffffffffu, there))
+      return false;
     g = ring[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&g_empty[slot]);
@@ -437,12 +443,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     constexpr int kTwo = kEpiWarps / 4;
     const int w = warp & 3, half = tid >> 7;
     bool ok = wait(l_full, seg - 1);
-    if (group_or<kEpiWarps>(2, !ok)) return false;
     const bool whole = g.t0 == 0 && g.t1 == g.tiles;
     // a piece: slot 0 of the CTA for its first segment's, 1 for its last's (an item's first piece)
     const int slot = 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0);
     const long long orow = (long long)g.s.b * P.c.N * P.H + g.s.f0, rows = (long long)P.c.B * P.c.N * P.H;
-    if (tid < kCols) {
+    if (ok && tid < kCols) {
       float l = 0.0f;
 #pragma unroll 4
       for (int i = 0; i < 16; ++i) l += fin[64 * i + tid];
@@ -459,7 +464,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
     }
     // (the sums are there before the last product over rows is done)
-    ok = wait(&pv_done[kl & 1], kl >> 1);
+    ok = ok && wait(&pv_done[kl & 1], kl >> 1);
     if (group_or<kEpiWarps>(2, !ok)) return false;
     tc_fence_after();
     if (lane == 0) mbar_arrive(l_empty);
@@ -639,6 +644,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // ticket sets the counter back.  A segment is
     // published one ahead of its queries' copy (64 rows of [B * N * H][D] from the item's first; rows past
     // its last are other sequences' or zeros: columns that nothing reads).
+#ifdef CSA_DEBUG_BOUNDS
+    if (P.test_late && lane == 0) {
+      const uint64_t t0 = globaltimer();
+      while (!*abort_flag && globaltimer() - t0 < 4 * kWait) {}
+    }
+    __syncwarp();
+#endif
     if (lane == 0) {
       const bool split = P.split;
       int item = first_item, tile = first_tile, drawn = 0, left = share, index = first_index;
@@ -947,9 +959,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i) m[i] = l[i] = 0.0f;
       const bool several = g.s.tlo != g.s.thi;  // tokens: their rows differ
-      if (several) {
-        if (threadIdx.x < kCols) colt[threadIdx.x] = min(g.s.thi, P.c.start + P.by_heads.of(g.s.f0 + (int)threadIdx.x));
-        group_sync(1);
+      if (several) {  // (every warp of a half writes its 32 positions, the same ones: no barrier for them)
+        const int f = 32 * hq + lane;
+        colt[f] = min(g.s.thi, P.c.start + P.by_heads.of(g.s.f0 + f));
+        __syncwarp();
       }
 #pragma unroll 1
       for (int t = g.t0; t < g.t1; ++t, ++k) {
@@ -1394,7 +1407,8 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
   P.by_page = Divisor(call.paged ? call.cache.page_size : 1);
 #ifdef CSA_DEBUG_BOUNDS
   P.test_stall = getenv("CSA_TEST_STALL_LAST_STAGE") != nullptr;
-  P.wait_ns = P.test_stall ? 200000000ull : kWaitNs;
+  P.test_late = getenv("CSA_TEST_LATE_SEGMENT") != nullptr;
+  P.wait_ns = P.test_stall || P.test_late ? 200000000ull : kWaitNs;
 #endif
   const long long units = attention_units(a, call);
   P.split = units > 0;
