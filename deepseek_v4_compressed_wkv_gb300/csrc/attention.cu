@@ -283,6 +283,12 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
+// Two e4m3 scales, the first in the low byte.  The caller's arrays may hold any byte: 0x7F and 0xFF are
+// NaN, and make the entry's block NaN.
+__device__ __forceinline__ float2 e4m3x2_values(uint32_t bytes) {
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)bytes, __NV_E4M3)));
+}
+
 // Eight e2m1 codes (element 0 in the low nibble) times a scale (bf16x2) to eight bf16.  The bytes of
 // a magnitude's bf16 pattern (0, .5, 1, 1.5, 2, 3, 4, 6) are looked up by byte permutation; products
 // of 2 and 4 significant bits are exact in bf16.
@@ -819,8 +825,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if ((int)u >= upr) continue;
             const uint32_t at = dst + (u >> 1) * kChunkBytes + r * 128;
             const uint32_t word[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
-            const float s0 = e4m3_value(sc[j] & 255u), s1 = e4m3_value(sc[j] >> 8);
-            const uint32_t s2[2] = {bf16x2(s0, s0), bf16x2(s1, s1)};
+            const float2 s = e4m3x2_values(sc[j]);
+            const uint32_t s2[2] = {bf16x2(s.x, s.x), bf16x2(s.y, s.y)};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const uint4 d = dequant8(word[q], s2[q >> 1]);

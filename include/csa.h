@@ -334,8 +334,8 @@ int csa_rope_table(const csa_options* opt, int pos0, int npos, float* cos_out, f
 
 /* A paged cache of entries (dev arrays owned by the caller): page p, slot s is row
  * p * page_size + s of each array, in csa_out's element layouts.  latent holds the entries' bf16
- * values; codes and scales hold e2m1 codes with e4m3 scales per 16 features (fp4 = 1) or
- * power-of-two scales per 32 (fp4 = 2).  Either may be absent (NULL).  Entry j of a sequence is
+ * values; codes and scales hold e2m1 codes with e4m3 scales per 16 features (fp4 = 1; the bytes 0x7F
+ * and 0xFF are NaN) or power-of-two scales per 32 (fp4 = 2).  Either may be absent (NULL).  Entry j of a sequence is
  * slot j % page_size of page page_table[sequence][j / page_size].  A compressed-KV cache written by
  * csa_compress_prefill_into is one too: page_size = cache_rows and page b for sequence b. */
 typedef struct {
