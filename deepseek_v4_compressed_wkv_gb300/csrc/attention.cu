@@ -984,7 +984,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(raw[i]);
         const int v0 = t * kTile, v1 = min(v0 + kTile, g.s.cnt), v = v0 + 16 * qt + (lane >> 2);
         bool renew = !ok || g.tiles == 1;
-        uint32_t spoilt = 0;  // bits 0, 1: this thread's rows hold a NaN or infinity that a token must not see
+        uint32_t spoilt = 0;  // bits 0, 1: this thread's rows may hold a NaN or infinity that a token must not see
         if (several) {
           // rows that only some of the item's tokens see
           const int begin = max(v0, P.sinks);
@@ -1005,13 +1005,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               if (rare) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                  float& y = x[4 * (i >> 1) + 2 * h + (i & 1)];
-                  // a score of -inf is a row with an infinity: NaN for a token that sees it
-                  if ((uint32_t)((i & 1 ? tc[i >> 1].y : tc[i >> 1].x) - j) < reach) {
-                    if (y == -INFINITY) y = __int_as_float(0x7fffffff);
-                  } else if (!(fabsf(y) < INFINITY)) {
-                    spoilt |= 1u << h;
-                  }
+                  // (a token that sees such a row gets NaN from any other score)
+                  const float y = x[4 * (i >> 1) + 2 * h + (i & 1)];
+                  const bool sees = (uint32_t)((i & 1 ? tc[i >> 1].y : tc[i >> 1].x) - j) < reach;
+                  if (sees ? y == -INFINITY : !(fabsf(y) < INFINITY)) spoilt |= 1u << h;
                 }
                 if (vv >= g.s.cnt) spoilt &= ~(1u << h);
               }
@@ -1053,9 +1050,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             break;
           }
           if (several) {
-            // a row that really holds a NaN or infinity is cleared: weight 0 times it is then 0
+            // a row that really holds a NaN or infinity is cleared: weight 0 times it is then 0.  For a token that
+            // sees it, its score is NaN; -inf from a finite row is the weight 0.
             spoilt |= __shfl_xor_sync(0xffffffffu, spoilt, 1);
             spoilt |= __shfl_xor_sync(0xffffffffu, spoilt, 2);
+            uint32_t cleared = 0;
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
               uint8_t* at = sC + (k & (nst - 1)) * stage_bytes + (16 * qt + (lane >> 2) + 8 * h) * 128 + (lane & 3) * 32;
@@ -1073,6 +1072,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < 8 * chunks; ++c)
                   *reinterpret_cast<volatile uint32_t*>(at + (c >> 3) * kChunkBytes + (c & 7) * 4) = 0u;
+              cleared |= bad << h;
+            }
+            if (cleared) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int vv = v + 8 * h, j = vv < P.sinks ? vv : vv + g.s.jump;
+                const uint32_t reach = P.window && vv >= P.sinks ? P.window : 0x7fffffffu;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if ((cleared >> h & 1) && (uint32_t)(colt[8 * (i >> 1) + c2 + (i & 1)] - j) < reach)
+                    x[4 * (i >> 1) + 2 * h + (i & 1)] = __int_as_float(0x7fffffff);
+              }
             }
           }
           // the queries' maxima over the tile, by way of the weights buffer (rows of 64): this thread's

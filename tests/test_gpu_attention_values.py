@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import deepseek_v4_compressed_wkv_gb300 as csa
-from test_gpu_attention import DEV, Pages, check, fp4_values, gen, reference
+from test_gpu_attention import DEV, Pages, check, fp4_values, gen, reference, visible
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,40 @@ def test_a_scale_that_is_not_a_number_shows(D, at, block, byte):
         short = torch.tensor([at, 300, 150], dtype=torch.int32, device=DEV)
         out, lse = a.decode(q, P.cache, P.table, short)
         check((out[0], lse[0]), reference(q[0], P.values[0][:at]))
+
+
+@pytest.mark.parametrize("H,D,window,sinks", [(64, 512, 40, 3), (8, 128, 40, 3), (16, 64, 0, 0), (33, 64, 70, 0), (1, 64, 20, 1)])
+def test_scores_below_f32_are_weight_0_in_every_tile(H, D, window, sinks):
+    """Rows of finite values whose scores pass f32's range downwards: exp(-inf) = 0, wherever in an item's
+    rows they lie (some of its tokens see them, or all)."""
+    N, g = 200, gen(H)
+    q, kv = torch.randn(1, N, H, D, generator=g, device=DEV).bfloat16(), torch.randn(1, N, D, generator=g, device=DEV).bfloat16()
+    q[..., 0], kv[..., 0] = 2.0 ** 66, 0
+    low = torch.tensor([1, 30, 31, 77, 120, 121, 199], device=DEV)
+    kv[0, low, 0] = -2.0 ** 66  # -2^132: f32 ends at 2^128
+    finite = torch.ones(N, dtype=torch.bool, device=DEV)
+    finite[low] = False
+    out, lse = csa.Attention(H, D, window, sinks).prefill(q, kv)
+    for t in range(N):
+        rows = visible(t, window, sinks).to(DEV)
+        check((out[0, t], lse[0, t]), reference(q[0, t], kv[0][rows[finite[rows]]]), f"token {t}")
+    cache, table = csa.PagedCache(kv.view(10, 20, D)), torch.arange(10, dtype=torch.int32, device=DEV)[None]
+    out, lse = csa.Attention(H, D).decode(q[:, 9], cache, table, torch.tensor([199], dtype=torch.int32, device=DEV))
+    check((out[0], lse[0]), reference(q[0, 9], kv[0, :199][finite[:199]]))
+
+
+@pytest.mark.parametrize("H", [8, 64])
+def test_an_infinity_in_a_row_does_not_pass_for_a_number(H):
+    """Its score is -inf for half of the heads: tokens that see the row get NaN in its feature at least, the
+    others do not."""
+    g = gen(H)
+    q, kv = torch.randn(1, 200, H, 64, generator=g, device=DEV).bfloat16(), torch.randn(1, 200, 64, generator=g, device=DEV).bfloat16()
+    a = csa.Attention(H, 64, 20, 3)
+    clean = a.prefill(q, kv)[0]
+    for at in (1, 50, 63, 64, 120, 199):
+        x = kv.clone()
+        x[0, at, 7] = -math.inf
+        out = a.prefill(q, x)[0]
+        see = torch.tensor([at in visible(t, 20, 3).tolist() for t in range(200)], device=DEV)
+        assert torch.equal(out[0][~see], clean[0][~see])
+        assert out[0][see][..., 7].isnan().all()
