@@ -69,7 +69,12 @@ constexpr int kCutMany = 8;  // units (see units_of) that cutting items costs: t
 constexpr int kCutFew = 3;   // and where the items are few
 constexpr float kStep = 16.0f;  // base-2 steps a score may pass the reference by
 constexpr float kLow = -64.0f;  // where the first scores are all lower, 0 is no reference for them
-constexpr float kFloor = -1e38f;  // the maximum of no scores
+constexpr float kFloor = -3.402823466e38f;  // the maximum of no scores
+// Base-2 scores from here on (either sign) have no digits behind the point, and x * scale - m, which is
+// rounded once, would be off by half a step of the reference m, up to any power of two: as maxima they
+// make the reference, and with it the result, NaN.  Below, that is a factor of 2^-32 to 2^32 common to all of a
+// query's weights.
+constexpr float kHuge = 1073741824.0f;
 constexpr int kAuxBytes = 6144;   // barriers, flags, references and sums
 
 // Division of 31-bit numbers by a number known to the host: with l = ceil(log2 d) and
@@ -1109,7 +1114,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               const int v = begin < P.sinks ? begin : max(begin, P.window ? tt - P.window + 1 - g.s.jump : 0);
               before = v < v0 && (v < P.sinks ? v : v + g.s.jump) <= tt;
             }
-            const float m0 = red[threadIdx.x], m1 = y * sl - m0 > kStep || (!before && y > kFloor && (y * sl < kLow || g.tiles == 1)) ? y * sl : m0;
+            const float m0 = red[threadIdx.x], top = fabsf(y * sl) < kHuge ? y * sl : __int_as_float(0x7fffffff);
+            const float m1 = y * sl - m0 > kStep || (!before && y > kFloor && (y * sl < kLow || g.tiles == 1)) ? top : m0;
             red[threadIdx.x] = m1;
             red[64 + threadIdx.x] = before ? ex2(m0 - m1) : 1.0f;
           }

@@ -329,8 +329,12 @@ int csa_rope_table(const csa_options* opt, int pos0, int npos, float* cos_out, f
  *   no visible j: out = 0, lse = -inf
  *
  * Scores, softmax statistics and sums are f32; the weights exp(S - m), m near the maximum, are
- * rounded to bf16 for the second product and out is rounded to bf16 once.  Rows that are not
- * visible to a query are not read for it: what they hold (NaN, infinities) cannot reach its result. */
+ * rounded to bf16 for the second product and out is rounded to bf16 once.  What a row holds (NaN,
+ * infinities) cannot reach the result of a query that does not see it (a prompt's kernel reads the
+ * rows of several tokens together, and clears such a row for those that do not see it).  A visible row
+ * with an infinity gives NaN in that feature at least.  A score of -inf, as products of finite values
+ * that pass f32's range downwards give, is the weight 0.  A maximum of S * log2(e) of 2^30 or more in
+ * size (scores without digits behind the point) gives NaN. */
 
 /* A paged cache of entries (dev arrays owned by the caller): page p, slot s is row
  * p * page_size + s of each array, in csa_out's element layouts.  latent holds the entries' bf16

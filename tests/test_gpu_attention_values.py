@@ -85,3 +85,73 @@ def test_an_infinity_in_a_row_does_not_pass_for_a_number(H):
         see = torch.tensor([at in visible(t, 20, 3).tolist() for t in range(200)], device=DEV)
         assert torch.equal(out[0][~see], clean[0][~see])
         assert out[0][see][..., 7].isnan().all()
+
+
+def sized(n, D, scores, seed):
+    """q [D], c [n, D] whose products are the given powers of two (times 1, 0 or -1 in c's bf16 values):
+    one feature holds them, the others of q are 0, of c random."""
+    c = torch.randn(n, D, generator=gen(seed), device=DEV).bfloat16()
+    q = torch.zeros(D, dtype=torch.bfloat16, device=DEV)
+    q[1] = 2.0 ** 14 if abs(scores).max() < 2 ** 60 else 2.0 ** 64
+    c[:, 1] = (scores / q[1].double()).bfloat16()
+    assert torch.equal(c[:, 1].double() * q[1].double(), scores)
+    return q, c
+
+
+def best(q, c, scale):
+    """The output, lse and sum of weighted magnitudes.  The scores are exact in f32, and of two that differ
+    by more than a few the smaller has the weight 0."""
+    s = c.double() @ q.double() * scale
+    p = torch.softmax(s, 0)
+    return p @ c.double(), torch.logsumexp(s, 0), p @ c.double().abs()
+
+
+def agrees(out, lse, ref):
+    mean, z, size = ref  # (a rounding of the weights, one of the output; the sums' f32 steps)
+    assert ((out.double() - mean).abs() <= 2.0 ** -8 * (size + mean.abs()) + 2.0 ** -12 * size).all()
+    assert ((lse.double() - z).abs() <= 2.0 ** -22 * z.abs() + 2.0 ** -12).all()
+
+
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 24, 2.0 ** 30, 2.0 ** 32, -2.0 ** 24, -2.0 ** 32])
+@pytest.mark.parametrize("n", [40, 300, 5000])
+def test_large_scores(n, size):
+    """Base-2 scores of up to 0.7 * 2^30: all equal; the larger ones first, last, and in one tile only."""
+    D, H = 64, 8
+    a, step = csa.Attention(H, D), abs(size) * 2.0 ** -7
+    near = torch.arange(n, device=DEV)
+    for k, up in enumerate((near < 0, near < n // 3, near >= n - 5, near == n // 2)):
+        q, c = sized(n, D, torch.where(up, size + step, size).double(), n + k)
+        qq, rows = q.expand(1, H, D).contiguous(), torch.zeros(-(-n // 64) * 64, D, dtype=torch.bfloat16, device=DEV)
+        rows[:n] = c
+        out, lse = a.decode(qq, csa.PagedCache(rows.view(-1, 64, D)), torch.arange(-(-n // 64), dtype=torch.int32, device=DEV)[None],
+                            torch.tensor([n], dtype=torch.int32, device=DEV))
+        ref = best(q, c, D ** -0.5)
+        agrees(out[0], lse[0], ref)
+        if n <= 300:
+            out, lse = a.prefill(q.expand(1, n, H, D).contiguous(), c[None])
+            for t in (0, 1, n // 3, n // 2, n - 5, n - 1):
+                agrees(out[0, t], lse[0, t], best(q, c[:t + 1], D ** -0.5))
+
+
+@pytest.mark.parametrize("size", [2.0 ** 34, 2.0 ** 60, -2.0 ** 34, -2.0 ** 60, -2.0 ** 127, 2.0 ** 127])
+def test_scores_without_digits_give_nan(size):
+    """Base-2 scores of 2^30 and more: never a finite result that is wrong."""
+    D, H, n = 64, 8, 200
+    q, c = sized(n, D, torch.full((n,), size, device=DEV, dtype=torch.float64), 1)
+    a = csa.Attention(H, D)
+    out, lse = a.prefill(q.expand(1, n, H, D).contiguous(), c[None])
+    assert out.isnan().all() and lse.isnan().all()
+    out, lse = a.decode(q.expand(1, H, D).contiguous(), csa.PagedCache(c[:192].view(3, 64, D).contiguous()),
+                        torch.arange(3, dtype=torch.int32, device=DEV)[None], torch.tensor([150], dtype=torch.int32, device=DEV))
+    assert out.isnan().all() and lse.isnan().all()
+
+
+def test_products_near_f32s_end_under_a_small_scale():
+    D, H, n = 64, 8, 300
+    for size in (-2.0 ** 127, 2.0 ** 127):
+        q, c = sized(n, D, torch.full((n,), size, device=DEV, dtype=torch.float64), 2)
+        a = csa.Attention(H, D, scale=1e-36)
+        out, lse = a.prefill(q.expand(1, n, H, D).contiguous(), c[None])
+        for t in (0, 1, 63, 64, 299):
+            mean, z, mag = best(q, c[:t + 1], float(torch.tensor(1e-36)))
+            agrees(out[0, t], lse[0, t], (mean, z, mag))
