@@ -126,11 +126,11 @@ __device__ __forceinline__ Seen seen_rows(const AttnParams& P, int item) {
   s.b = P.by_per.of(item);
   s.f0 = (item - s.b * P.per) * kCols;
   if (P.c.paged) {
-    const int top = P.c.max_pages * P.c.cache.page_size, n = __ldg(P.c.lens + s.b);
+    const int top = P.c.max_pages * P.c.cache.page_size, n = P.c.lens[s.b];
     s.cols = min(kCols, P.H - s.f0);
     s.tlo = s.thi = min(max(n, 0), top) - 1;
   } else {
-    const int n = P.c.lens ? min(max(__ldg(P.c.lens + s.b), 0), P.c.N) : P.c.N;
+    const int n = P.c.lens ? min(max(P.c.lens[s.b], 0), P.c.N) : P.c.N;
     s.cols = max(0, min(kCols, n * P.H - s.f0));
     s.tlo = P.c.start + P.by_heads.of(s.f0);
     s.thi = P.c.start + P.by_heads.of(s.f0 + max(s.cols, 1) - 1);
@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int j = v < P.sinks ? v : v + g.s.jump;
       if (!P.c.paged) return g.s.b * P.c.kv_rows + j;
       const int ps = P.c.cache.page_size, pg = P.by_page.of(j);
-      const int page = __ldg(P.c.page_table + (long long)g.s.b * P.c.max_pages + pg);
+      const int page = P.c.page_table[(long long)g.s.b * P.c.max_pages + pg];
       if (page >= 0 && page < P.c.cache.pages) return page * ps + (j - pg * ps);
       atomicOr(P.flag, 2);
       return -1;
@@ -817,8 +817,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const bool live = rr >= 0 && u0 + 4 * j < upr;
-              code[j] = live ? __ldg(cp + 4 * j) : make_uint4(0, 0, 0, 0);
-              sc[j] = live ? __ldg(sp + 4 * j) : 0;
+              code[j] = live ? cp[4 * j] : make_uint4(0, 0, 0, 0);
+              sc[j] = live ? sp[4 * j] : 0;
             }
           }
           look_ahead(t + 1);

@@ -31,9 +31,18 @@ struct AppendParams {
 
 template <class T>
 __device__ __forceinline__ void copy_units(uint8_t* dst, const uint8_t* src, int bytes, int lane) {
-#pragma unroll 4
-  for (int i = lane; i < bytes / (int)sizeof(T); i += 32)
-    reinterpret_cast<T*>(dst)[i] = __ldg(reinterpret_cast<const T*>(src) + i);
+  // (units loaded before the first store: the entries may be the cache's own memory as far as the compiler knows)
+  constexpr int kAhead = 4;
+  const int n = bytes / (int)sizeof(T);
+  for (int i = lane; i < n; i += 32 * kAhead) {
+    T v[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (i + 32 * j < n) v[j] = reinterpret_cast<const T*>(src)[i + 32 * j];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (i + 32 * j < n) reinterpret_cast<T*>(dst)[i + 32 * j] = v[j];
+  }
 }
 
 __device__ __forceinline__ void copy_row(uint8_t* dst, const uint8_t* src, int bytes, int unit, int lane) {
@@ -173,8 +182,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(const NormParams P) {
     const int f = 8 * (i * T + t);
     const bool act = live && f < P.dim;
     const float4* gp = reinterpret_cast<const float4*>(P.gain + f);
-    g[i][0] = act ? __ldg(gp) : make_float4(0, 0, 0, 0);
-    g[i][1] = act ? __ldg(gp + 1) : make_float4(0, 0, 0, 0);
+    g[i][0] = act ? gp[0] : make_float4(0, 0, 0, 0);
+    g[i][1] = act ? gp[1] : make_float4(0, 0, 0, 0);
   }
   float s[PIECES][8];
   float ss = 0.0f;

@@ -31,7 +31,9 @@ size_t attention_workspace_bytes(int head_dim);
 // one, griddep_wait, before it touches memory): 2 of the 10 us that a small kernel takes in a stream.
 // Such a kernel lets its own successor be set up only behind its wait, so that a kernel that has
 // started finds everything before its direct predecessor complete (the compressor's decode reads its
-// weights, and then its state, before it waits).
+// weights, and then its state, before it waits).  What it reads may be written by that launch while it
+// already runs: such a kernel takes it by ordinary loads behind its wait, never by the non-coherent path
+// (__ldg), which is for data that does not change during the kernel's life.
 template <class... Params>
 cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                          const std::remove_cv_t<Params>&... params) {
