@@ -101,8 +101,11 @@ class PagedCache:
         self._struct = _Cache(*ptr, self.pages, self.page_size, D, fp4)
         self._ref = ctypes.addressof(self._struct)
         self._arrays = [t for t in (latent, codes, scales) if t is not None]
-        # made here: an append on another stream, or in a captured graph, must not have to clear it
+        # Cleared here, and done when this returns: an append on another stream, or in a captured graph, must
+        # not have to do it, nor its bits be cleared afterwards.
         self._flag = torch.zeros(1, dtype=_I32, device=base.device)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(base.device).synchronize()
         self._append = load_library().csa_cache_append
 
     @classmethod
@@ -150,12 +153,16 @@ class PagedCache:
         if rc < 0:
             _check(rc, "csa_cache_append")
 
-    def status(self):
+    def status(self, stream=None):
         """Raises CSAError if an append since the last call left an entry out (a negative index, an
-        index beyond the page table, or a page outside the cache)."""
-        bits = int(self._flag.item())
-        if bits:
+        index beyond the page table, or a page outside the cache).  Reads and clears the cache's status
+        word on the current stream or on ``stream``, and waits for it: appends on other streams have to
+        be ordered before it (events, wait_stream), like all work on one cache."""
+        with torch.cuda.stream(stream):
+            seen = self._flag.clone()
             self._flag.zero_()
+            bits = int(seen.item())
+        if bits:
             what = [w for b, w in ((1, "a negative index"), (2, "an index beyond the page table"),
                                    (4, "a page outside the cache")) if bits & b]
             raise CSAError("append left entries out: " + ", ".join(what))
