@@ -5,8 +5,9 @@ csrc/_build/, then linked into csrc/_build/libcsa.so.  Nothing is installed.
 
 build(variant="bounds") builds the bounds-checked library instead (csrc/_build_bounds/,
 -DCSA_DEBUG_BOUNDS): every kernel store with a computed index is checked against its buffer's
-extent, skipped if outside and reported through the handle's device flag (bit 8).  The tests
-run the parity cases against it; the binding loads it when CSA_LIBRARY_VARIANT=bounds.
+extent, skipped if outside and reported: through the handle's device flag (bit 8), the cache
+write's status word (bit 8), or the norm's return value.  The tests run the parity cases and those of the
+attention layer against it; the binding loads it when CSA_LIBRARY_VARIANT=bounds.
 """
 from __future__ import annotations
 

@@ -106,11 +106,24 @@ struct AttnParams {
   bool split;        // items may be cut (the join kernel follows); else they are drawn from `ticket`
   int* ticket;       // items drawn beyond each CTA's first; 0 between calls
 #ifdef CSA_DEBUG_BOUNDS
-  uint64_t wait_ns;  // the time-out test shortens the waits
-  int test_stall;    // and leaves out each CTA's first tile
-  int test_late;     // or publishes each CTA's first segment only once a wait for it has run out
+  long long rows, slots;  // extents of the outputs and of the workspace's pieces (and records)
+  uint64_t wait_ns;       // the time-out tests shorten the waits
+  int test_stall;         // and leave out each CTA's first tile
+  int test_late;          // or publish each CTA's first segment only once a wait for it has run out
 #endif
 };
+
+// The bounds-checked build's checks of a store: to row `row` of the outputs, to element i of the pieces,
+// their statistics or the records, `per` of which make a slot.
+#ifdef CSA_DEBUG_BOUNDS
+__device__ __forceinline__ bool in_rows(const AttnParams& P, long long row) { return in_bounds(row, P.rows, P.flag); }
+__device__ __forceinline__ bool in_slots(const AttnParams& P, long long i, long long per) {
+  return in_bounds(i, P.slots * per, P.flag);
+}
+#else
+__device__ __forceinline__ bool in_rows(const AttnParams&, long long) { return true; }
+__device__ __forceinline__ bool in_slots(const AttnParams&, long long, long long) { return true; }
+#endif
 
 // ---- the rows an item sees
 struct Seen {
@@ -457,7 +470,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const bool whole = g.t0 == 0 && g.t1 == g.tiles;
     // a piece: slot 0 of the CTA for its first segment's, 1 for its last's (an item's first piece)
     const int slot = 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0);
-    const long long orow = (long long)g.s.b * P.c.N * P.H + g.s.f0, rows = (long long)P.c.B * P.c.N * P.H;
+    const long long orow = (long long)g.s.b * P.c.N * P.H + g.s.f0;
     if (ok && tid < kCols) {
       float l = 0.0f;
 #pragma unroll 4
@@ -468,9 +481,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(l));
         asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(l));
         inv[tid] = l == 0.0f ? 0.0f : r;
-        if (P.c.lse && tid < g.s.cols && in_bounds(orow + tid, rows, P.flag))
+        if (P.c.lse && tid < g.s.cols && in_rows(P, orow + tid))
           P.c.lse[orow + tid] = l == 0.0f ? -INFINITY : (m + lg) * 0.693147180559945f;
-      } else {
+      } else if (in_slots(P, slot * kCols + tid, kCols)) {
         P.part_ml[slot * kCols + tid] = make_float2(l == 0.0f ? kFloor : m, l);  // (no row: no reference either)
       }
     }
@@ -486,7 +499,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     };
     const uint32_t base = tmem + ((uint32_t)(32 * w) << 16);
     if (whole) {
-      if (P.split && P.few && tid == 0) P.record[g.item] = make_int2(-1, 0);
+      if (P.split && P.few && tid == 0 && in_slots(P, g.item, 1)) P.record[g.item] = make_int2(-1, 0);
       // steps of 32 queries x 32 features (16 of a last block of 64) a warp; the next step's loads run
       // ahead of a step's stores
       const int steps = (chunks + 1) & ~1;  // two of a block
@@ -544,7 +557,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
             const int q = 32 * c + 16 * i + 8 * z + (lane >> 2);
-            if ((full || (lane & 3) < 2) && q < g.s.cols && in_bounds(orow + q, rows, P.flag))
+            if ((full || (lane & 3) < 2) && q < g.s.cols && in_rows(P, orow + q))
               *reinterpret_cast<uint4*>(dst + (16 * i + 8 * z) * 2 * D) = y[z];
           }
         }
@@ -558,7 +571,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tmem_ld_frag(base + (x >> 1) * kCols + ((uint32_t)(16 * (x & 1)) << 16), o);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          dst[(x * 32 + i) * 32] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+          if (in_slots(P, (dst - P.part) + (x * 32 + i) * 32, kCols * D / 4)) dst[(x * 32 + i) * 32] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         }
         if (kTwo == 2 || (x & 1)) give_back(x >> 1);
@@ -568,7 +581,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int last = g.index + g.tiles, each = work[0], more = work[1], wide = more * (each + 1);
         const int j = last < wide ? last / (each + 1) : more + (last - wide) / each;
         const int n = j - (int)blockIdx.x + 1;
-        P.record[P.few ? g.item : blockIdx.x] = make_int2(P.few ? (int)blockIdx.x : g.item, n);
+        const int at = P.few ? g.item : (int)blockIdx.x;
+        if (in_slots(P, at, 1)) P.record[at] = make_int2(P.few ? (int)blockIdx.x : g.item, n);
       }
     }
     return true;
@@ -646,7 +660,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       if (lane == 0) {
         work[0] = each, work[1] = more;  // (read by whoever leaves an item's first piece)
-        if (!P.few) P.record[blockIdx.x] = make_int2(-1, 0);
+        if (!P.few && in_slots(P, blockIdx.x, 1)) P.record[blockIdx.x] = make_int2(-1, 0);
       }
     }
     // ---- scheduling and queries (one lane).  A split call's segments are the CTA's share; otherwise
@@ -1325,13 +1339,13 @@ __global__ void __launch_bounds__(kLanes * kGroups, 1024 / (kLanes * kGroups)) a
       }
     }
   }
-  const long long orow = (long long)s.b * P.c.N * P.H + s.f0, rows = (long long)P.c.B * P.c.N * P.H;
+  const long long orow = (long long)s.b * P.c.N * P.H + s.f0;
   const float i0 = y.y == 0.0f ? 0.0f : 1.0f / y.y, i1 = y.w == 0.0f ? 0.0f : 1.0f / y.w;
   if (grp == 0 && P.c.lse && j0 - threadIdx.x < 256 && lane < 4) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float t = e ? y.w : y.y;
-      if (q + e < s.cols && in_bounds(orow + q + e, rows, P.flag))
+      if (q + e < s.cols && in_rows(P, orow + q + e))
         P.c.lse[orow + q + e] = t == 0.0f ? -INFINITY : ((e ? y.z : y.x) + log2f(t)) * 0.693147180559945f;
     }
   }
@@ -1351,7 +1365,7 @@ __global__ void __launch_bounds__(kLanes * kGroups, 1024 / (kLanes * kGroups)) a
     // features 16 w of the last 64, else 32 w + 16 (x % 2) of 128
     const int d = (x | 1) < P.D / 64 ? (x >> 1) * 128 + 32 * w + 16 * (x & 1) : x * 64 + 16 * w;
     const int t = threadIdx.x >> 1, u = threadIdx.x & 1;
-    if (grp == 0 && t < kLanes / 4 && q0 + t < s.cols && in_bounds(orow + q0 + t, rows, P.flag))
+    if (grp == 0 && t < kLanes / 4 && q0 + t < s.cols && in_rows(P, orow + q0 + t))
       *reinterpret_cast<uint4*>(P.c.out + (orow + q0 + t) * P.D + d + 8 * u) = *reinterpret_cast<const uint4*>(&tile[t][8 * u]);
     __syncthreads();
   }
@@ -1429,6 +1443,9 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
   P.by_heads = Divisor(P.H);
   P.by_page = Divisor(call.paged ? call.cache.page_size : 1);
 #ifdef CSA_DEBUG_BOUNDS
+  const char* shorter = getenv("CSA_TEST_SHORT_EXTENTS");  // the test of the checks: "rows" or "slots"
+  P.rows = (long long)call.B * call.N * a->heads - (shorter && *shorter == 'r' ? 1 : 0);
+  P.slots = shorter && *shorter == 's' ? 1 : slots;
   P.test_stall = getenv("CSA_TEST_STALL_LAST_STAGE") != nullptr;
   P.test_late = getenv("CSA_TEST_LATE_SEGMENT") != nullptr;
   P.wait_ns = P.test_stall || P.test_late ? 200000000ull : kWaitNs;

@@ -229,6 +229,11 @@ int csa_rmsnorm_residual_q8(const uint16_t* x, const uint16_t* residual, const f
   CSA_CUDA(csa::launch_rmsnorm_residual_q8(x, residual, gain, rows, dim, eps, scale_block, residual_out, y, q, scales,
                                            (cudaStream_t)stream),
            "rmsnorm launch");
+#ifdef CSA_DEBUG_BOUNDS
+  int flag = 0;
+  CSA_CUDA(csa::take_norm_flag((cudaStream_t)stream, &flag), "rmsnorm bounds flag");
+  if (flag) return fail(CSA_ERR_DEVICE, "%s: index out of bounds (bounds-checked build)", what);
+#endif
   return CSA_OK;
 }
 

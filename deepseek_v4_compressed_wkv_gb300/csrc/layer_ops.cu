@@ -1,4 +1,6 @@
 // The paged cache's write and the residual RMSNorm with an 8-bit output.
+#include <cstdlib>
+
 #include "layer_ops.h"
 #include "tc_common.cuh"
 
@@ -27,6 +29,9 @@ struct AppendParams {
   int B, G, max_pages;
   int lat_unit, code_unit, scale_unit;  // bytes moved at a time: 16, 8, 4, 2 or 1
   int lat_bytes, code_bytes, scale_bytes;
+#ifdef CSA_DEBUG_BOUNDS
+  long long rows;  // of the cache
+#endif
 };
 
 template <class T>
@@ -81,6 +86,12 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const A
     return;
   }
   const long long row = (long long)p * size + (j - page * size);
+#ifdef CSA_DEBUG_BOUNDS
+  if (row < 0 || row >= P.rows) {  // (the status word, where the caller has one, stands in for a handle's flag)
+    if (P.status && lane == 0) atomicOr(P.status, 8);
+    return;
+  }
+#endif
   if (P.cache.latent)
     copy_row((uint8_t*)P.cache.latent + row * P.lat_bytes, (const uint8_t*)P.in.latent + (size_t)e * P.lat_bytes, P.lat_bytes,
              P.lat_unit, lane);
@@ -121,7 +132,21 @@ struct NormParams {
   long long rows;
   int dim;
   float eps;
+#ifdef CSA_DEBUG_BOUNDS
+  long long extent;  // rows that the outputs have
+#endif
 };
+
+// The bounds-checked build's check of a store to element i of an output of `per` elements a row; the
+// operator has no handle whose flag could be raised, so this build keeps one of its own.
+#ifdef CSA_DEBUG_BOUNDS
+__device__ int norm_flag;
+__device__ __forceinline__ bool in_output(const NormParams& P, long long i, long long per) {
+  return in_bounds(i, P.extent * per, &norm_flag);
+}
+#else
+__device__ __forceinline__ bool in_output(const NormParams&, long long, long long) { return true; }
+#endif
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -202,7 +227,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(const NormParams P) {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       const int f = 8 * (i * T + t);
-      if (live && f < P.dim)
+      if (live && f < P.dim && in_output(P, base + f, P.dim))
         __stcs(reinterpret_cast<uint4*>(P.residual_out + base + f),
                make_uint4(bf_pack(s[i][0], s[i][1]), bf_pack(s[i][2], s[i][3]), bf_pack(s[i][4], s[i][5]),
                           bf_pack(s[i][6], s[i][7])));
@@ -227,7 +252,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(const NormParams P) {
       s[i][k] = s[i][k] * inv * gk[k];
       amax[i] = max_nan(amax[i], fabsf(s[i][k]));
     }
-    if (P.y && live && f < P.dim)
+    if (P.y && live && f < P.dim && in_output(P, base + f, P.dim))
       __stcs(reinterpret_cast<uint4*>(P.y + base + f),
              make_uint4(bf_pack(s[i][0], s[i][1]), bf_pack(s[i][2], s[i][3]), bf_pack(s[i][4], s[i][5]),
                         bf_pack(s[i][6], s[i][7])));
@@ -260,11 +285,12 @@ __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(const NormParams P) {
       a = __fdiv_rn(max_nan(m, kAmaxFloor), kE4m3Max);
     if (!live || f >= P.dim) continue;
     if (BLOCK == 32) {
-      if ((t & (kLanes - 1)) == 0)
+      if ((t & (kLanes - 1)) == 0 && in_output(P, row * (P.dim / 32) + f / 32, P.dim / 32))
         reinterpret_cast<uint8_t*>(P.scales)[row * (P.dim / 32) + f / 32] = (uint8_t)byte;
     } else if (BLOCK == 128) {
-      if ((t & (kLanes - 1)) == 0) reinterpret_cast<float*>(P.scales)[row * (P.dim / 128) + f / 128] = a;
-    } else if (f == 0) {
+      if ((t & (kLanes - 1)) == 0 && in_output(P, row * (P.dim / 128) + f / 128, P.dim / 128))
+        reinterpret_cast<float*>(P.scales)[row * (P.dim / 128) + f / 128] = a;
+    } else if (f == 0 && in_output(P, row, 1)) {
       reinterpret_cast<float*>(P.scales)[row] = a;
     }
     // One reciprocal for the block's quotients: 2^-126 <= a <= 2^120, so it is a normal number.
@@ -273,7 +299,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(const NormParams P) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       w[k] = __nv_cvt_float2_to_fp8x2(make_float2(s[i][2 * k] * back, s[i][2 * k + 1] * back), __NV_SATFINITE, __NV_E4M3);
-    __stcs(reinterpret_cast<uint2*>(P.q + base + f), make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16)));
+    if (in_output(P, base + f, P.dim))
+      __stcs(reinterpret_cast<uint2*>(P.q + base + f), make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16)));
   }
 }
 
@@ -302,6 +329,9 @@ cudaError_t launch_cache_append(const csa_cache& cache, const csa_out& in, int B
   P.B = B;
   P.G = G;
   P.max_pages = max_pages;
+#ifdef CSA_DEBUG_BOUNDS
+  P.rows = cache.pages * cache.page_size - (getenv("CSA_TEST_SHORT_EXTENTS") ? 1 : 0);
+#endif
   P.lat_bytes = cache.head_dim * 2;
   P.code_bytes = cache.head_dim / 2;
   P.scale_bytes = cache.head_dim / fp4_scale_block(cache.fp4);
@@ -316,7 +346,25 @@ cudaError_t launch_rmsnorm_residual_q8(const uint16_t* x, const uint16_t* residu
                                        int dim, float eps, int scale_block, uint16_t* residual_out, uint16_t* y,
                                        uint8_t* q, void* scales, cudaStream_t s) {
   NormParams P{x, residual, gain, residual_out, y, q, scales, rows, dim, eps};
+#ifdef CSA_DEBUG_BOUNDS
+  P.extent = rows - (getenv("CSA_TEST_SHORT_EXTENTS") ? 1 : 0);
+#endif
   return scale_block == 32 ? launch_norm<32>(P, s) : scale_block == 128 ? launch_norm<128>(P, s) : launch_norm<0>(P, s);
 }
+
+#ifdef CSA_DEBUG_BOUNDS
+// Reads and clears the flag behind the stream's work; 0 while the stream is captured.
+cudaError_t take_norm_flag(cudaStream_t s, int* flag) {
+  *flag = 0;
+  cudaStreamCaptureStatus capture;
+  cudaError_t e = cudaStreamIsCapturing(s, &capture);
+  if (e != cudaSuccess || capture != cudaStreamCaptureStatusNone) return e;
+  const int zero = 0;
+  e = cudaMemcpyFromSymbolAsync(flag, norm_flag, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && *flag) e = cudaMemcpyToSymbolAsync(norm_flag, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+  return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
+}
+#endif
 
 }  // namespace csa

@@ -56,6 +56,9 @@ cudaError_t launch_cache_append(const csa_cache& cache, const csa_out& in, int B
 cudaError_t launch_rmsnorm_residual_q8(const uint16_t* x, const uint16_t* residual, const float* gain, long long rows,
                                        int dim, float eps, int scale_block, uint16_t* residual_out, uint16_t* y,
                                        uint8_t* q, void* scales, cudaStream_t s);
+#ifdef CSA_DEBUG_BOUNDS
+cudaError_t take_norm_flag(cudaStream_t s, int* flag);  // the norm's stores outside their outputs
+#endif
 
 }  // namespace csa
 

@@ -164,7 +164,8 @@ class PagedCache:
             bits = int(seen.item())
         if bits:
             what = [w for b, w in ((1, "a negative index"), (2, "an index beyond the page table"),
-                                   (4, "a page outside the cache")) if bits & b]
+                                   (4, "a page outside the cache"),
+                                   (8, "a store outside the cache (bounds-checked build)")) if bits & b]
             raise CSAError("append left entries out: " + ", ".join(what))
 
 

@@ -359,7 +359,8 @@ typedef struct {
  *  first       [B] int32 dev: index of the sequence's first new entry
  *  mask        [B] u8 dev or NULL (all): e.g. the emitted flags of a decode step
  *  status      one int dev or NULL: bits are set (never cleared) where an entry was left out: 1 a
- *              negative index, 2 an index beyond the page table, 4 a page outside the cache
+ *              negative index, 2 an index beyond the page table, 4 a page outside the cache (8, only in
+ *              the bounds-checked build: a store outside the cache, skipped)
  * head_dim must be a multiple of 16 in [16, 512].  Two entries of one call for the same slot race.
  * Returns CSA_OK or a negative csa_status. */
 int csa_cache_append(const csa_cache* cache, const csa_out* in, int B, int G, const int32_t* page_table, int max_pages,
@@ -435,7 +436,8 @@ void csa_attention_destroy(csa_attention* a);
  * a NaN or an infinity gives what the formula gives (NaN; a NaN block has a NaN scale, e8m0 byte
  * 255).
  * Requirements: dim a multiple of scale_block and of 32, at most 16384; arrays 16-byte aligned
- * (scales 4).  rows may be 0 (nothing is enqueued). */
+ * (scales 4).  rows may be 0 (nothing is enqueued).  (The bounds-checked build waits for the
+ * stream, unless it is captured, and returns CSA_ERR_DEVICE where a store was outside its output.) */
 int csa_rmsnorm_residual_q8(const uint16_t* x, const uint16_t* residual, const float* gain, int64_t rows, int dim,
                             float eps, int scale_block, uint16_t* residual_out, uint16_t* y, uint8_t* q, void* scales,
                             csa_stream_t stream);

@@ -1,6 +1,8 @@
-"""Cases of the attention layer's operators that only the bounds-checked build of the library can run
-(its test hooks), in a child process with CSA_LIBRARY_VARIANT=bounds (the library is loaded once per
-process)."""
+"""Cases of the attention layer's operators on the bounds-checked build of the library
+(-DCSA_DEBUG_BOUNDS): every store with a computed index of the attention's kernels (outputs, pieces,
+their statistics, records), of the cache write and of the norm is checked, left out where it is outside,
+and reported.  Some cases need the build's test hooks.  They run in child processes with
+CSA_LIBRARY_VARIANT=bounds (the library is loaded once per process)."""
 import os
 import subprocess
 import sys
@@ -27,3 +29,11 @@ def run_on_the_bounds_checked_build(*files):
 
 def test_segments_published_late():
     run_on_the_bounds_checked_build("test_gpu_attention_late.py")
+
+
+def test_the_checks_themselves():
+    run_on_the_bounds_checked_build("test_gpu_layer_extents.py")
+
+
+def test_values_and_streams():
+    run_on_the_bounds_checked_build("test_gpu_attention_values.py", "test_gpu_layer_streams.py")
