@@ -88,7 +88,8 @@ int csa_attention_create(int heads, int head_dim, int window, int sinks, float s
   if (head_dim < 64 || head_dim > 512 || head_dim % 64)
     return fail(CSA_ERR_ARG, "head_dim %d must be a multiple of 64 in [64, 512]", head_dim);
   if (window < 0 || sinks < 0) return fail(CSA_ERR_ARG, "window (%d) and sinks (%d) must be >= 0", window, sinks);
-  if (!(scale >= 0.0f) || std::isinf(scale)) return fail(CSA_ERR_ARG, "scale must be finite and >= 0");
+  if (!(scale >= 0.0f) || std::isinf((float)(scale * 1.4426950408889634)))
+    return fail(CSA_ERR_ARG, "scale must be >= 0 and, times log2(e), finite");
   auto* a = new (std::nothrow) csa_attention();
   if (!a) return fail(CSA_ERR_INTERNAL, "out of host memory");
   a->heads = heads;

@@ -372,7 +372,7 @@ typedef struct csa_attention csa_attention;
  * the last `window` positions (0: all) and the first `sinks` positions always visible (no effect
  * without a window).  scale multiplies the scores; 0 selects 1 / sqrt(head_dim).
  * Requirements: 1 <= heads <= 1024, head_dim a multiple of 64 in [64, 512], window >= 0,
- * sinks >= 0, scale finite and >= 0.
+ * sinks >= 0, scale >= 0 and finite, also times log2(e).
  * Allocates the workspace for split sequences on the current device, which becomes the handle's
  * device.  Calls allocate nothing afterwards and can be captured into CUDA graphs after a first
  * call on the device.  A handle's calls share its workspace: order them on the device (one stream,
