@@ -201,7 +201,8 @@ class Attention:
     def prefill(self, q, kv, start_pos: int = 0, lens=None, out=None, lse=None, stream=None):
         """q bf16 [B, N, heads, head_dim]: tokens start_pos .. of each sequence; kv bf16 [B, rows,
         head_dim], rows >= start_pos + N; lens int32 [B]: tokens of each sequence in a padded batch
-        (outputs of the others are left as they were).  Returns (out bf16 like q, lse f32 [B, N, heads])."""
+        (outputs of the others are left as they were).  Returns (out bf16 like q, lse f32 [B, N, heads]).
+        No sequences or no tokens: nothing is done."""
         if q.dim() != 4 or kv.dim() != 3:
             raise CSAError("q must be [B, N, heads, head_dim] and kv [B, rows, head_dim]")
         B, N = q.shape[0], q.shape[1]
@@ -213,6 +214,8 @@ class Attention:
         kp = _want("kv", kv, _BF16, (B, kv.shape[1], self.head_dim), dev)
         lp = None if lens is None else _want("lens", lens, _I32, (B,), dev)
         op, out, zp, lse, s = self._outputs(q, out, lse, shape, lshape, dev, stream, (q, kv, lens, out, lse))
+        if B == 0 or N == 0:
+            return out, lse
         rc = self._lib.csa_attention_prefill(self._h, qp, kp, B, N, start_pos, kv.shape[1], lp, op, zp, s)
         if rc < 0:
             _check(rc, "csa_attention_prefill")
@@ -236,7 +239,7 @@ class Attention:
     def decode(self, q, cache: PagedCache, page_table, lens, out=None, lse=None, stream=None):
         """q bf16 [B, heads, head_dim]: one new token a sequence, at position lens[b] - 1 (lens int32
         [B] on the device) of its entries in the cache; page_table int32 [B, max_pages].  Returns
-        (out bf16 like q, lse f32 [B, heads])."""
+        (out bf16 like q, lse f32 [B, heads]).  No sequences: nothing is done."""
         if q.dim() != 3 or page_table.dim() != 2:
             raise CSAError("q must be [B, heads, head_dim] and page_table [B, max_pages]")
         B = q.shape[0]
@@ -250,6 +253,8 @@ class Attention:
         lp = _want("lens", lens, _I32, (B,), dev)
         op, out, zp, lse, s = self._outputs(q, out, lse, shape, lshape, dev, stream,
                                             (q, page_table, lens, out, lse, *cache._arrays))
+        if B == 0:
+            return out, lse
         rc = self._lib.csa_attention_decode(self._h, qp, cache._ref, pp, width, lp, B, op, zp, s)
         if rc < 0:
             _check(rc, "csa_attention_decode")
