@@ -444,14 +444,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // The next segment, for every role but the scheduling warp; false behind the last one and after an
   // abort.  The softmax's and the epilogue's warps meet at named barriers, which have no time limit, and
   // after an abort one of them may still find a slot written that another has given up on: they go on or
-  // leave by their group's common decision, all others by the warp's own.
+  // leave by their group's common decision (the epilogue's here, the softmax's at its first tile's barrier,
+  // which costs it none), all others by the warp's own.
   uint32_t seg = 0;  // segments read
   Segment g;
   auto next = [&]() {
     const uint32_t slot = seg % kRing;
     const bool there = wait(&g_full[slot], seg / kRing);
-    if (warp < kEpiWarp ? group_or(1, !there) : warp < kMmaWarp ? group_or<kEpiWarps>(2, !there) : !__all_sync(0xffffffffu, there))
+    if (warp >= kEpiWarp && warp < kMmaWarp ? group_or<kEpiWarps>(2, !there) : !__all_sync(0xffffffffu, there)) {
+      g.t1 = -1;
       return false;
+    }
     g = ring[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&g_empty[slot]);
@@ -979,7 +982,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const float sl = P.scale_log2;
     uint32_t k = 0;
     bool ok = true;
-    while (ok && next()) {
+    for (;;) {
+      if (!next()) {
+        // the two barriers that a warp which has the segment comes to when its first tile has failed
+        if (group_or(1, g.t1 < 0)) group_or(1, true);
+        break;
+      }
       float m[8], l[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) m[i] = l[i] = 0.0f;
