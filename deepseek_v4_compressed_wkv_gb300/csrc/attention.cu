@@ -25,16 +25,20 @@
 // A tile passes four stations one after the other, its copy, the scores (1100), the softmax (1200)
 // and the values (900), and shared memory holds two tiles of 512 features beside the queries, so two
 // tiles go through them at a time:
-//   decode over latents  3200 cycles a tile, 0.87 of HBM's rate while tiles stream; 128 sequences of up
-//                        to 2048 entries, 64 heads of 512: 47.6 us in all (152 MB, 3.2 TB/s), of which 4
+//   decode over latents  3200 cycles a tile, 0.78 of that rate while tiles stream; 128 sequences of up
+//                        to 2048 entries, 64 heads of 512: 48.9 us in all (152 MB, 3.1 TB/s), of which 4
 //                        pass before the first copy (lengths, shares, page table: one after the other),
 //                        2.3 until it lands, 2.5 in the last pieces' stores and 8.5 in their join
-//   decode over codes    3750 cycles a tile, 1900 of them the expansion of codes to bf16: 49.0 us
+//   decode over codes    3750 cycles a tile, 1900 of them the expansion of codes to bf16 (736 are its
+//                        instructions' issue, the rest latencies with two of these warps a scheduler):
+//                        50.1 us, 0.9 of it gained since by the hardware's conversion of the scales
 //   a prompt's window    7400 cycles an item of two tiles: the epilogue reads O^T for 5000 of them, which
 //                        the next item's values wait for block by block (there is no room for a second
-//                        O^T at D = 512): 4096 tokens, 64 heads of 512, window 128: 112.6 us (542 MB, 4.8 TB/s)
+//                        whole O^T at D = 512; two of its four blocks would fit, which is not built): 4096
+//                        tokens, 64 heads of 512, window 128: 112.4 us (542 MB, 4.8 TB/s)
 //   narrow heads         1250 cycles a tile at D = 128, the softmax alone: 2 x 1777 tokens, 16 heads, window
-//                        512: 45.2 us
+//                        512: 45.1 us (0.3 of it the look at rows whose scores pass f32's range)
+// (times: a call in a graph of 16 or 64 of them over changing inputs)
 //
 // Measured and not taken: stages handed over by blocks of 128 features (decode 128 x 2048 1 % faster, a
 // windowed prompt 2 to 8 % and codes 4 % slower); products over rows in steps that leave out a last

@@ -14,8 +14,8 @@ using namespace tcx;
 //
 // Bytes are moved once; one warp per entry, each array's row as units of the widest type its
 // addresses allow (a 512-wide latent is two 16-byte units a lane).  8 x 2048 latents of 512 features
-// (33.6 MB) take 8 us in a stream, which is also what a call costs its host; a decode step's 128
-// entries are bound by the launch.  Entries and indices fit 32 bits: with 64-bit quotients the kernel
+// (33.6 MB) take 8.1 us in a graph of calls, which is also what a call costs its host; a decode step's 128
+// entries 1.9 us, bound by the launch.  Entries and indices fit 32 bits: with 64-bit quotients the kernel
 // ran twice as many instructions (10.2 us with them and without the early start).  Asking for the
 // latent before its slot is looked up measured the same.
 
@@ -116,10 +116,10 @@ int common_unit(const void* a, const void* b, int bytes) {
 // the products with a scale's reciprocal are f32.
 //
 // 9 bytes a feature move through HBM, which bounds it: 16461 rows of 4096 with scales per 128 take
-// 95 us (607 MB, 6.4 TB/s, 95 % of a copy's).  Every load of a thread is asked for before the first value is used:
+// 95 us (609 MB, 6.4 TB/s, 95 % of a copy's).  Every load of a thread is asked for before the first value is used:
 // with each piece's residual stored before the next piece's loads, and eight divisions a piece, the
 // same rows took 112 us.  Two pieces a thread: one (512 threads, two CTAs' worth of them waiting at
-// each reduction) takes 134 us, four (a third of the warps) 114 us.  Few rows are bound by the launch.
+// each reduction) takes 134 us, four (a third of the warps) 114 us.  128 rows take 2.8 us in a graph of calls, bound by the launch.
 
 struct NormParams {
   const uint16_t* x;

@@ -374,7 +374,8 @@ typedef struct csa_attention csa_attention;
  * Requirements: 1 <= heads <= 1024, head_dim a multiple of 64 in [64, 512], window >= 0,
  * sinks >= 0, scale >= 0 and finite, also times log2(e).
  * Allocates the workspace for split sequences on the current device, which becomes the handle's
- * device.  Calls allocate nothing afterwards and can be captured into CUDA graphs after a first
+ * device: 128 bytes * SMs * (4 * head_dim + 8) and a little (40 MB at 512 features).  Layers of the same
+ * options that run one after the other can share a handle, and with it the workspace.  Calls allocate nothing afterwards and can be captured into CUDA graphs after a first
  * call on the device.  A handle's calls share its workspace: order them on the device (one stream,
  * or events; graphs captured from one handle are replayed one after the other). */
 int csa_attention_create(int heads, int head_dim, int window, int sinks, float scale, csa_attention** out);
@@ -422,7 +423,8 @@ int64_t csa_attention_launches(const csa_attention* a);
 void csa_attention_destroy(csa_attention* a);
 
 /* Residual addition, RMSNorm and quantisation to 8 bits of rows of a token stream, in one pass:
- *   s = x + residual (f32);  n = s * (mean(s^2) + eps)^-1/2 * gain
+ *   s = x + residual (f32);  n = s * (mean(s^2) + eps)^-1/2 * gain  (the mean in f32: a row whose sum of
+ *   squares passes 3.4e38 gets the factor 0)
  *   residual_out = bf16(s), y = bf16(n), q = e4m3(n / a), scales = a of each block
  *  x, residual   [rows][dim] bf16 dev; residual may be NULL (s = x)
  *  gain          [dim] f32 dev
