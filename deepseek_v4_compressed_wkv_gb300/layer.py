@@ -222,14 +222,16 @@ class PageTable:
             raise CSAError("pages, sequences, max_pages and page_size must be below 2^31")
         n = _check(self._lib.csa_pages_workspace(self.pages, self.sequences, self.max_pages), "csa_pages_workspace")
         self._work = torch.empty(n, dtype=_I32, device=refs.device)
-        self._flag = torch.zeros(1, dtype=_I32, device=refs.device)
-        if not torch.cuda.is_current_stream_capturing():  # (as a cache's)
-            torch.cuda.current_stream(refs.device).synchronize()
         ints = functools.partial(torch.zeros, dtype=_I32, device=refs.device)
         n, most = self.sequences, max(1, self.pages // 2)
+        self._flag = ints(1)
         self._rows, self._first = (n,), ints(n)
         self._forks = _split(ints(2 * n + 1), (n, n, 1))
         self._moves = _split(ints(2 * most + 1), (most, most, 1))
+        # All of them are there when this returns (as a cache's word): a step on another stream must not find a fill
+        # behind it, which would take its count and lists back.
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(refs.device).synchronize()
         self._at = [t.data_ptr() for t in (self._first, *self._forks, *self._moves)]
         self._struct = _Pages(*ptr, self._work.data_ptr(), self._flag.data_ptr(), self.pages, self.sequences, self.max_pages,
                               page_size)
