@@ -1596,11 +1596,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attention_merge_kernel(const
   const long long rows = (long long)P.c.B * P.H, row = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
   if (row >= rows) return;
   const int b = P.by_heads.of((int)row), n = length_of(P, b), sh = shared_by(P, b, n);
-  // (a part that the call has not written is not read)
+  // (a part that the call has not written is not read; one whose weights are all 0 is: 0 times an infinity shows)
+  const bool there0 = sh > 0, there1 = n > sh || n == 0;
   const float2 none = make_float2(kFloor, 0.0f);
-  const float2 y0 = sh > 0 ? P.c.part_ml[row] : none, y1 = n > sh || n == 0 ? P.c.part_ml[rows + row] : none;
+  const float2 y0 = there0 ? P.c.part_ml[row] : none, y1 = there1 ? P.c.part_ml[rows + row] : none;
   const float m = fmaxf(y0.x, y1.x), w0 = ex2(y0.x - m) * y0.y, w1 = ex2(y1.x - m) * y1.y, sum = w0 + w1;
-  const bool there0 = y0.y != 0.0f, there1 = y1.y != 0.0f;
   const float f0 = sum == 0.0f ? 0.0f : w0 / sum, f1 = sum == 0.0f ? 0.0f : w1 / sum;
   const float4* a = reinterpret_cast<const float4*>(P.c.part + row * P.D);
   const float4* c = reinterpret_cast<const float4*>(P.c.part + (rows + row) * P.D);
