@@ -1009,13 +1009,30 @@ cudaError_t launch_linear_q8(const uint8_t* q, const float* a, const uint8_t* w,
                    : launch_tile<128>(q, w, P, s);
 }
 
+// Takes away the bits that were seen: a call on another stream may have raised one since, which is left to the next look.
+// (The same bit raised again before it is taken away is reported by the look that had seen it.)
+__global__ void clear_linear_flag_kernel(int seen) {
+  griddep_wait();
+  griddep_launch_dependents();
+  atomicAnd(&linear_flag, ~seen);
+}
+
 // Reads and clears the device's flag behind the stream's work.
 cudaError_t take_linear_flag(cudaStream_t s, int* flag) {
   *flag = 0;
-  const int zero = 0;
   cudaError_t e = cudaMemcpyFromSymbolAsync(flag, linear_flag, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && *flag) e = cudaMemcpyToSymbolAsync(linear_flag, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+  if (e != cudaSuccess || !*flag) return e;
+#ifdef CSA_DEBUG_BOUNDS
+  // the test of this: a bit is raised between the look and the clearing
+  if (const char* bits = getenv("CSA_TEST_RAISE_BEFORE_CLEARING")) {
+    const int more = *flag | atoi(bits);
+    e = cudaMemcpyToSymbolAsync(linear_flag, &more, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    if (e != cudaSuccess) return e;
+  }
+#endif
+  clear_linear_flag_kernel<<<1, 1, 0, s>>>(*flag);
+  e = cudaGetLastError();
   return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
 }
 

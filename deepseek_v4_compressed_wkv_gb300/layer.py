@@ -504,7 +504,8 @@ def linear_q8(q, scales, weight, weight_scales, dtype=_BF16, out=None, stream=No
 
 
 def linear_q8_status(stream=None):
-    """Raises CSAError if a linear_q8 on the current device since the last call ran out of a wait's time.  Reads
-    and clears the device's flag on the current stream or on ``stream``, and waits for it."""
+    """Raises CSAError if a linear_q8 on the current device, from any thread or stream, since the last call ran out of
+    a wait's time.  Reads and clears the device's flag on the current stream or on ``stream``, and waits for it: calls
+    still running on other streams are the next look's."""
     s = _raw_stream(_current_device()) if stream is None else stream.cuda_stream
     _check(load_library().csa_linear_q8_status(s), "csa_linear_q8_status")

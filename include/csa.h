@@ -545,7 +545,8 @@ int csa_linear_q8(const uint8_t* q, const float* scales, const uint8_t* weight, 
 
 /* Reads and clears the current device's flag of csa_linear_q8 (synchronises the stream): CSA_OK,
  * CSA_ERR_TIMEOUT (a device-side wait ran out in some call since the last look; its output is undefined) or,
- * in the bounds-checked build, CSA_ERR_DEVICE (a store outside the output, skipped). */
+ * in the bounds-checked build, CSA_ERR_DEVICE (a store outside the output, skipped).  The flag is that of all the
+ * device's calls, whichever thread or stream made them: what is still running may raise it for the next look. */
 int csa_linear_q8_status(csa_stream_t stream);
 
 #ifdef __cplusplus
