@@ -62,13 +62,18 @@ int check_cache(const csa_cache* c, const char* what) {
   return CSA_OK;
 }
 
+// The steps' loops go up to 256 pages, slots or sequences past the last one before they end, as ints.
+constexpr long long kMostPages = 0x7fffffffLL - 1023;
+
 int check_pages(const csa_pages* t, const char* what) {
   if (!t) return fail(CSA_ERR_ARG, "%s: the page table is NULL", what);
   if (t->pages < 1 || t->sequences < 1 || t->max_pages < 1 || t->page_size < 1)
     return fail(CSA_ERR_ARG, "%s: pages (%d), sequences (%d), max_pages (%d) and page_size (%d) must be >= 1", what, t->pages,
                 t->sequences, t->max_pages, t->page_size);
-  if ((long long)t->sequences * t->max_pages > 0x7fffffffLL || (long long)t->max_pages * t->page_size > 0x7fffffffLL)
-    return fail(CSA_ERR_ARG, "%s: sequences * max_pages and max_pages * page_size must be below 2^31", what);
+  if (t->pages > kMostPages || (long long)t->sequences * t->max_pages > kMostPages)
+    return fail(CSA_ERR_ARG, "%s: pages and sequences * max_pages must be at most 2^31 - 1024", what);
+  if ((long long)t->max_pages * t->page_size > 0x7fffffffLL)
+    return fail(CSA_ERR_ARG, "%s: max_pages * page_size must be below 2^31", what);
   if (!t->refs || !t->table || !t->lens || !t->workspace)
     return fail(CSA_ERR_ARG, "%s: refs, table, lens and workspace are required", what);
   return CSA_OK;
@@ -296,8 +301,8 @@ int csa_rmsnorm_residual_q8(const uint16_t* x, const uint16_t* residual, const f
 }
 
 int64_t csa_pages_workspace(int pages, int sequences, int max_pages) {
-  if (pages < 1 || sequences < 1 || max_pages < 1 || (long long)sequences * max_pages > 0x7fffffffLL)
-    return fail(CSA_ERR_ARG, "csa_pages_workspace: pages (%d), sequences (%d) and max_pages (%d) must be >= 1, sequences * max_pages below 2^31",
+  if (pages < 1 || sequences < 1 || max_pages < 1 || pages > kMostPages || (long long)sequences * max_pages > kMostPages)
+    return fail(CSA_ERR_ARG, "csa_pages_workspace: pages (%d), sequences (%d) and max_pages (%d) must be >= 1, pages and sequences * max_pages at most 2^31 - 1024",
                 pages, sequences, max_pages);
   return csa::pages_workspace_ints(pages, sequences, max_pages);
 }

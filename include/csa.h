@@ -487,7 +487,8 @@ int csa_cache_copy_pages(const csa_cache* cache, const int32_t* src, const int32
  *   lens   [sequences]              entries
  * The first ceil(lens / page_size) slots of a row are in use.  A page that several sequences have is full and
  * nobody writes to it: only a sequence's own last page and new ones take entries.
- * Pages are handed out lowest first, in the sequences' order; every result is the same at each run. */
+ * Pages are handed out lowest first, in the sequences' order; every result is the same at each run.
+ * All four numbers >= 1, pages and sequences * max_pages at most 2^31 - 1024, max_pages * page_size below 2^31. */
 typedef struct {
   int32_t* refs;
   int32_t* table;  /* also the page_table of csa_cache_append and csa_attention_decode */
