@@ -174,8 +174,8 @@ class PagedCache:
         dev = _current_device()
         if self.device != dev:
             raise CSAError(f"the cache is on cuda:{self.device}, but the current CUDA device is cuda:{dev}")
-        if src.dim() != 1:
-            raise CSAError(f"src must be [n], got {tuple(src.shape)}")
+        if src.dim() != 1 or src.shape[0] >= 2 ** 31:
+            raise CSAError(f"src must be [n], n below 2^31, got {tuple(src.shape)}")
         sp, dp = _want("src", src, _I32, src.shape, dev), _want("dst", dst, _I32, src.shape, dev)
         cp = None if count is None else _want("count", count, _I32, (1,), dev)
         if stream is None:
@@ -375,8 +375,8 @@ class Attention:
         groups int32 [G + 1] with shared int32 [G], 1 <= G <= B: sequences groups[g] .. groups[g + 1] - 1 have their
         first shared[g] entries in common (the full pages that PageTable.fork shares), which are then read with all
         of the group's queries together.  Only without a window."""
-        if q.dim() != 3 or page_table.dim() != 2:
-            raise CSAError("q must be [B, heads, head_dim] and page_table [B, max_pages]")
+        if q.dim() != 3 or page_table.dim() != 2 or page_table.shape[1] >= 2 ** 31:
+            raise CSAError("q must be [B, heads, head_dim] and page_table [B, max_pages], max_pages below 2^31")
         B = q.shape[0]
         dev = _current_device()
         if cache.device != dev:
@@ -439,8 +439,8 @@ def rmsnorm_residual_q8(x, residual, gain, eps: float = 1e-6, scale_block: int =
     dim = shape[-1]
     if scale_block not in (0, 32, 128):
         raise CSAError(f"scale_block must be 0, 32 or 128, got {scale_block}")
-    if dim == 0 or dim % (128 if scale_block == 128 else 32):
-        raise CSAError(f"the last dimension must be a multiple of {128 if scale_block == 128 else 32}, got {dim}")
+    if dim == 0 or dim % (128 if scale_block == 128 else 32) or dim >= 2 ** 31:
+        raise CSAError(f"the last dimension must be a multiple of {128 if scale_block == 128 else 32} below 2^31, got {dim}")
     if inplace and residual is None:
         raise CSAError("inplace writes over a residual: none was given")
     dev = _current_device()
@@ -471,8 +471,8 @@ def linear_q8(q, scales, weight, weight_scales, dtype=_BF16, out=None, stream=No
     if weight.dim() != 2 or q.dim() < 1:
         raise CSAError("q must be [.., K] and weight [N, K]")
     N, K = weight.shape
-    if K == 0 or K % 128:
-        raise CSAError(f"the last dimension must be a positive multiple of 128, got {K}")
+    if K == 0 or K % 128 or K >= 2 ** 31:
+        raise CSAError(f"the last dimension must be a positive multiple of 128 below 2^31, got {K}")
     if dtype is not _BF16 and dtype is not _F32:
         raise CSAError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
     blocks = K // 128

@@ -24,3 +24,29 @@ def test_the_largest_page_tables_have_a_workspace():
     lib = csa.load_library()
     assert lib.csa_pages_workspace(MOST, 1, 1) > MOST
     assert lib.csa_pages_workspace(1, 1, MOST) > MOST and lib.csa_pages_workspace(1, MOST, 1) > MOST
+
+
+def meta(*shape, dtype):
+    import torch
+    return torch.empty(*shape, dtype=dtype, device="meta")
+
+
+def test_sizes_that_the_library_would_take_for_smaller_ones(monkeypatch):
+    """The library's counts are 32-bit: 2^32 + 128 features passed on as they are would be 128."""
+    import torch
+    from deepseek_v4_compressed_wkv_gb300 import layer
+    e4m3, i32, far = torch.float8_e4m3fn, torch.int32, 2 ** 32 + 128
+    monkeypatch.setattr(layer, "_current_device", lambda: 0)
+    cache = layer.PagedCache.__new__(layer.PagedCache)
+    cache.device = 0
+    attention = layer.Attention.__new__(layer.Attention)
+    attention.heads, attention.head_dim, attention._h = 16, 64, None
+    list_ = meta(far, dtype=i32)
+    q, row, lens = meta(1, 16, 64, dtype=torch.bfloat16), meta(1, far, dtype=i32), meta(1, dtype=i32)
+    for f in (lambda: csa.linear_q8(meta(1, far, dtype=e4m3), meta(1, far // 128, dtype=torch.float32), meta(1, far, dtype=e4m3),
+                                    meta(1, far // 128, dtype=torch.float32)),
+              lambda: cache.copy_pages(list_, list_), lambda: attention.decode(q, cache, row, lens),
+              lambda: attention.decode(q, cache, row, lens, groups=meta(2, dtype=i32), shared=meta(1, dtype=i32)),
+              lambda: csa.rmsnorm_residual_q8(meta(1, far, dtype=torch.bfloat16), None, meta(far, dtype=torch.float32))):
+        with pytest.raises(csa.CSAError, match="2.31"):
+            f()
