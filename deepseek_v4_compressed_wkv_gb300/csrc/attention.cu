@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // of the swizzled rows once: rows r and r + 4 side by side for 16-byte units, eight rows for units
     // that expand to 64 bytes
     const int r8 = kFp4 ? lane & 7 : (lane >> 3) + 4 * ((lane >> 2) & 1), u0 = kFp4 ? lane >> 3 : lane & 3;
-    constexpr int kGroups = kTileRows / 8;  // (latents)
+    constexpr int kEights = kTileRows / 8;  // (latents)
     // a cache's rows are read once by a call: they are not to drive pieces out of L2
     const uint64_t policy = P.c.paged && !kShared ? l2_evict_first() : l2_evict_normal();
     uint32_t k = 0;
@@ -1060,7 +1060,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             continue;
           }
 #pragma unroll 1
-          for (int i = 0; i < kGroups; ++i) {
+          for (int i = 0; i < kEights; ++i) {
             const int r = kTileRows * w + 8 * i + r8, ra = __shfl_sync(0xffffffffu, e0, r & 31),
                       rb = __shfl_sync(0xffffffffu, e1, r & 31), rr = r < 32 ? ra : rb;
             const uint32_t bytes = rr < 0 ? 0u : 16u;
