@@ -917,8 +917,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // that expand to 64 bytes
     const int r8 = kFp4 ? lane & 7 : (lane >> 3) + 4 * ((lane >> 2) & 1), u0 = kFp4 ? lane >> 3 : lane & 3;
     constexpr int kEights = kTileRows / 8;  // (latents)
-    // a cache's rows are read once by a call: they are not to drive pieces out of L2
-    const uint64_t policy = P.c.paged && !kShared ? l2_evict_first() : l2_evict_normal();
+    // A cache's rows are read once by a call: they are not to drive pieces out of L2.  Not so the rows that groups share,
+    // which every sequence of a group finds there (us with evict_first and without, 64 heads: 128 x (8192 + 512) entries of
+    // 512 features in one group 181.0 and 178.7, in 8 groups 184.8 and 182.3, in 16, 134 MB, 187.3 and 186.4, 64 x (32768 + 512)
+    // in 2 332.6 and 327.7; with 256 features, where stages are handed over whole, 87.9 and 88.4).
+    const uint64_t policy = P.c.paged && !kShared && !kFine ? l2_evict_first() : l2_evict_normal();
     uint32_t k = 0;
     int pending = -1;  // a stage whose copies were issued and not yet handed over
     bool ok = true;
