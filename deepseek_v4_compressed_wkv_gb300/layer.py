@@ -266,7 +266,7 @@ class PageTable:
         return self._first
 
     def fork(self, parent, stream=None):
-        """Sequence i becomes what sequence parent[i] was (int32 [sequences]; -1: it ends, its pages are free).  Full
+        """Sequence i becomes what sequence parent[i] was (int32 [sequences]; negative: it ends, its pages are free).  Full
         pages are shared, each page that is not full stays with one heir.  Returns (src, dst, count), the copies
         that every cache then has to make: cache.copy_pages(*table.fork(parent))."""
         s = _raw_stream(self.device) if stream is None and _current_device() == self.device else self._step(stream, parent)

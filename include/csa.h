@@ -512,7 +512,7 @@ int64_t csa_pages_workspace(int pages, int sequences, int max_pages);
 int csa_pages_extend(const csa_pages* t, const int32_t* more, int32_t* first, csa_stream_t stream);
 
 /* Sequence i becomes what sequence parent[i] was (int32 [sequences] dev): forks one into several, reorders them,
- * or ends one, with parent[i] = -1 (a parent out of range is taken as -1 and raises bit 2).  parent[i] = i leaves it.
+ * or ends one, with a negative parent[i] (so does a parent of sequences or more, which raises bit 2).  parent[i] = i leaves it.
  * Full pages are shared.  A last page that is not full stays with the sequence itself or, if that gave way, with its
  * lowest heir; each other heir gets a page of its own and, in the heirs' order, an entry of the list of copies that
  * the caches then have to make:

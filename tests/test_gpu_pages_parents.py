@@ -1,0 +1,24 @@
+"""A fork's parents at the ends of their range: a negative one ends the sequence and is no error, one past the last
+sequence ends it too and is one."""
+import pytest
+
+import deepseek_v4_compressed_wkv_gb300 as csa
+from test_gpu_pages import dev, listed
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("sequences", [3, 100])  # one CTA, a cluster
+@pytest.mark.parametrize("parent,told", [(-1, False), (-2, False), (-7, False), (-2 ** 31, False), (None, True), (2 ** 31 - 1, True)])
+def test_a_sequence_ends(sequences, parent, told):
+    t = csa.PageTable.allocate(3 * sequences, sequences, 4, 2)
+    t.extend(dev([5] + [0] * (sequences - 2) + [3]))
+    parents = list(range(sequences))
+    parents[-1] = sequences if parent is None else parent
+    assert listed(t.fork(dev(parents))) == []
+    assert t.lens.tolist() == [5] + [0] * (sequences - 1) and t.refs.tolist() == [1, 1, 1] + [0] * (3 * sequences - 3)
+    assert t.table[-1].tolist() == [-1] * 4
+    if told:
+        with pytest.raises(csa.CSAError, match="argument"):
+            t.status()
+    t.status()
