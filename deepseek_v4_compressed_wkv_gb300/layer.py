@@ -200,7 +200,7 @@ class PagedCache:
             what = [w for b, w in ((1, "a negative index"), (2, "an index beyond the page table"),
                                    (4, "a page outside the cache"),
                                    (8, "a store outside the cache (bounds-checked build)")) if bits & b]
-            raise CSAError("append left entries out: " + ", ".join(what))
+            raise CSAError("append left entries out, or copy_pages pages: " + ", ".join(what))
 
 
 class PageTable:

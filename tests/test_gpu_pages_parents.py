@@ -1,5 +1,5 @@
-"""A fork's parents at the ends of their range: a negative one ends the sequence and is no error, one past the last
-sequence ends it too and is one."""
+"""What pages' steps and copies say of their arguments.  A fork's parents at the ends of their range: a negative one ends the
+sequence and is no error, one past the last sequence ends it too and is one."""
 import pytest
 
 import deepseek_v4_compressed_wkv_gb300 as csa
@@ -22,3 +22,11 @@ def test_a_sequence_ends(sequences, parent, told):
         with pytest.raises(csa.CSAError, match="argument"):
             t.status()
     t.status()
+
+
+def test_the_cache_names_the_call_that_left_a_page_out():
+    c = csa.PagedCache.allocate(4, 2, 64)
+    c.copy_pages(dev([1, 9]), dev([2, 3]))
+    with pytest.raises(csa.CSAError, match="copy_pages .*outside"):
+        c.status()
+    c.status()
