@@ -188,8 +188,9 @@ __device__ __forceinline__ Seen seen_front(const AttnParams& P, int item) {
     // ended ones before it cost each item a trip to L2 each: 3000 sequences, 100 of them alive, 1936 us)
     const int last = b0 + P.by_heads.of(min(f + kCols, all) - 1);
     s.b = b0 + P.by_heads.of(f);
-    while (s.b < last && length_of(P, s.b) < sh) ++s.b;
-    if (length_of(P, s.b) >= sh) s.cols = min(kCols, all - f);
+    int n;
+    while ((n = length_of(P, s.b)) < sh && s.b < last) ++s.b;
+    if (n >= sh) s.cols = min(kCols, all - f);
     s.cnt = sh;
     s.f0 = b0 * P.H + f;
   }
