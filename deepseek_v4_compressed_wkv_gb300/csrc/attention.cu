@@ -1658,6 +1658,10 @@ static long long shared_items(const csa_attention* a, const AttnCall& call) {
 // saved: 16 heads of 512, 32 sequences of 2048 entries 31 and 30, 4.8, of 4096 36 and 40, 9.6; 128 of 512 28 and 19, 4.8,
 // of 1024 33 and 40, 9.8, of 4096 50 and 104, 40; 300 of 512 45 and 33, 11; 16 heads of 128, 128 of 1024 22 and 19, 9.8, of
 // 2048 26 and 28, 20; 32 heads of 256, 128 of 2048 32 and 31, 13, 300 of 1024 38 and 40, 15.)
+// The lengths are on the device, so it is the page table that counts, and the rule is off where sequences are much shorter
+// than that or several tiles a sequence are all but full: 16 heads of 512, tables of 16384 entries, 128 of 512 36 and 27,
+// 300 of 512 43 and 48, 32 of 2048 31 and 30; 100 heads, 128 of 2048 101 and 94; 48 heads, 61 and 58.  Codes, which it was
+// not made on: 128 of 512 42 and 32, 300 of 512 44 and 57, 128 of 1024 35 and 48, 32 of 2048 32 and 34, 48 heads 70 and 66.
 bool shared_pays(const csa_attention* a, int B, int G, long long capacity) {
   const long long tiles = (capacity + kTile - 1) / kTile, own = (long long)B * ((a->heads + kCols - 1) / kCols);
   const long long front = (long long)B * a->heads / kCols + G;
@@ -1685,7 +1689,7 @@ cudaError_t launch_attention(csa_attention* a, const AttnCall& call, cudaStream_
   const Shape sh = attn_shape(a->D);
   // Calls whose sequences share rows read them from L2, where a tile's arrival is latency: handing stages over and back
   // by blocks of 128 features shortens it (us without and with, 64 heads: 128 x (8192 + 512) entries of 512 features 195
-  // and 180, of 384 156 and 149, of 128 the same, 32 x (8192 + 100) of 128 31 and 29), but not at 256 features, whose four
+  // and 179, of 384 156 and 149, of 128 the same, 32 x (8192 + 100) of 128 31 and 29), but not at 256 features, whose four
   // stages of two blocks only cost more barriers (87 and 102).  Pages that do not hold whole tiles bring rows one by
   // one, and lose by it (512 features, pages of 63: 216 and 228).
   const bool fine = call.G && !fp4 && a->D % 128 == 0 && a->D != 256 && call.cache.page_size % kTile == 0;

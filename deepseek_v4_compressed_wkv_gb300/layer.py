@@ -374,7 +374,9 @@ class Attention:
 
         groups int32 [G + 1] with shared int32 [G], 1 <= G <= B: sequences groups[g] .. groups[g + 1] - 1 have their
         first shared[g] entries in common (the full pages that PageTable.fork shares), which are then read with all
-        of the group's queries together.  Only without a window."""
+        of the group's queries together where the number of heads and the table's width promise that it pays.  The
+        sequences' lengths are not known here: few shared entries in a wide table can take longer than without groups
+        (figures in include/csa.h).  Only without a window."""
         if q.dim() != 3 or page_table.dim() != 2 or page_table.shape[1] >= 2 ** 31:
             raise CSAError("q must be [B, heads, head_dim] and page_table [B, max_pages], max_pages below 2^31")
         B = q.shape[0]
@@ -467,7 +469,7 @@ def rmsnorm_residual_q8(x, residual, gain, eps: float = 1e-6, scale_block: int =
 def linear_q8(q, scales, weight, weight_scales, dtype=_BF16, out=None, stream=None):
     """q float8_e4m3fn [.., K] with scales f32 [.., K / 128] (as rmsnorm_residual_q8 leaves them with scale_block
     128) times weight float8_e4m3fn [N, K] with weight_scales f32 [ceil(N / 128), K / 128]: dtype bf16 or f32
-    [.., N].  No rows or no columns: nothing is done."""
+    [.., N].  A row's last bits may depend on the number of rows.  No rows or no columns: nothing is done."""
     if weight.dim() != 2 or q.dim() < 1:
         raise CSAError("q must be [.., K] and weight [N, K]")
     N, K = weight.shape

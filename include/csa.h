@@ -411,20 +411,27 @@ int csa_attention_decode(csa_attention* a, const uint16_t* q, const csa_cache* c
                          int max_pages, const int32_t* lens, int B, uint16_t* out, float* lse, csa_stream_t stream);
 
 /* The same for sequences that share their first entries (answers sampled from one prompt, questions about one
- * document, a common system prompt): what csa_attention_decode gives.  Where it pays (fewer than 64 heads, where a
- * sequence alone does not fill a tile, and long page tables), the shared rows are multiplied by the queries of all of a
- * group's sequences together, in full tiles of 64 queries; else every sequence has its rows by itself, the shared ones
- * from L2.
+ * document, a common system prompt): what csa_attention_decode gives.  Where the page tables are long and a number of
+ * heads that is not a multiple of 64 leaves a sequence's tiles of 64 queries unfilled, the shared rows are multiplied by
+ * the queries of all of a group's sequences together, in full tiles; else every sequence has its rows by itself, the
+ * shared ones from L2 (a little faster than without groups for latents in pages of whole tiles of 64 entries, the same
+ * for others and for codes).
+ * The choice goes by the page table's length, since the sequences' are on the device: with few or short shared entries
+ * in a long table, or with more than 64 heads, a call can take longer than csa_attention_decode (16 heads of 512, 128
+ * sequences of 512 shared and 64 own entries in a table of 16384: 36 us and 27; of 4096 shared ones 52 and 103; 100
+ * heads, 2048 shared: 101 and 94).
  *  groups     [G + 1] int32 dev: group g is sequences groups[g] .. groups[g + 1] - 1; they do not descend and
  *             stay within [0, B].  A sequence outside every group shares nothing
  *  shared     [G] int32 dev: entries at the beginning that the group's sequences have in common (e.g. the full pages
- *             of a prompt that csa_pages_fork left them): read on the pages of one of its sequences of that length.  A
+ *             of a prompt that csa_pages_fork left them): read on the pages of any of its sequences that long.  A
  *             sequence shorter than that is taken by itself
  *  workspace  csa_attention_shared_workspace bytes dev, 16-byte aligned (NULL where that is 0); nothing is kept there
  *             between calls
  * The handle must have no window.  groups or shared out of range are taken as the nearest end and raise flag bit 1;
  * groups that descend raise it too and leave the results undefined.  The shared and the own rows' results are f32 and
- * joined by their maxima and sums.  1 <= G <= B, B * heads < 2^30; the rest as csa_attention_decode.
+ * joined by their maxima and sums.  1 <= G <= B, B * heads < 2^30; the rest as csa_attention_decode, where the shared
+ * rows' tiles count besides if the workspace is needed: (B * ceil(heads / 64) + B * heads / 64 + G) *
+ * (max_pages * page_size / 64 + 2) < 2^31.
  * Returns CSA_OK or a negative csa_status. */
 int csa_attention_decode_shared(csa_attention* a, const uint16_t* q, const csa_cache* cache, const int32_t* page_table,
                                 int max_pages, const int32_t* lens, int B, const int32_t* groups, const int32_t* shared, int G,
@@ -535,7 +542,8 @@ int csa_pages_compact(const csa_pages* t, int32_t* src, int32_t* dst, int32_t* c
  *  weight         [N][K] e4m3 dev
  *  weight_scales  [ceil(N / 128)][K / 128] f32 dev: one per block of 128 x 128 of the weight
  *  out            [T][N] bf16 dev, or f32 with out_f32 = 1; rounded once (bf16) or not (f32)
- * The products are exact, the two scales' product and every sum f32.  A NaN among a row's values or scales makes what it enters NaN, and
+ * The products are exact, the two scales' product and every sum f32.  A row's result is the same at every call of the
+ * same T, N and K; its last bits may differ between calls of different T, whose sums over K are split otherwise.  A NaN among a row's values or scales makes what it enters NaN, and
  * so does an infinite scale of a block whose sum is 0.
  * Requirements: K a positive multiple of 128, 1 <= N <= 2^31 - 128, 0 <= T < 2^22 (T = 0: nothing is enqueued),
  * ceil(T / 16) * ceil(N / 128) below 2^28;
