@@ -541,13 +541,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // Calls with shared rows: each item's tiles, worked out by a thread each and kept where the first tile's weights
   // come later (the scheduling warp alone took 9 us to look for 169 items' groups, twice).  Where there is no room for
   // them all, a thread leaves the sum and the longest of a part of what a scheduling lane goes through: warp w
-  // the w-th of kParts (3400 sequences of 2048 shared and 64 own entries, 16 heads: 793 -> 555 us).
+  // the w-th of kParts (3400 sequences of 2048 shared and 64 own entries, 16 heads: 793 -> 555 us).  (The lanes' ranges are
+  // worked out here and again by the scheduling warp: once for both, they cost the other calls up to 1 %.)
   constexpr int kParts = kAttnThreads / 32;
   int* const listed = reinterpret_cast<int*>(sP);
   const bool list = kShared && P.split && P.items <= 2 * kPBytes / (int)sizeof(int);
-  const int per = (P.items + 31) / 32, part = (per + kParts - 1) / kParts;  // items of a scheduling lane, of a part
-  const int lo = min(P.items, per * lane), hi = min(P.items, lo + per);
   if constexpr (kShared) {
+    const int per = (P.items + 31) / 32, part = (per + kParts - 1) / kParts;  // items of a scheduling lane, of a part
+    const int lo = min(P.items, per * lane), hi = min(P.items, lo + per);
     for (int i = threadIdx.x; list && i < P.items; i += kAttnThreads) listed[i] = tiles_of(seen_shared(P, i));
     if (P.split && !list) {
       int sum = 0, top = 0;
@@ -749,6 +750,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (P.split) {
       // ---- the CTA's share of the call's units: every CTA's scheduling warp adds up the items' (lanes over
       // contiguous items; the other roles' instructions arrive meanwhile) and finds its first one
+      const int per = (P.items + 31) / 32, lo = min(P.items, per * lane), hi = min(P.items, lo + per);
+      [[maybe_unused]] const int part = (per + kParts - 1) / kParts;
       int sum = 0, top = 0;  // (the host has made sure that the call's units fit)
       if (kShared && !list) {
         for (int i = 0; i < kParts; ++i) {
