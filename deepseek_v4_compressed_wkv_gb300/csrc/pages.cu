@@ -296,7 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const __grid_co
     if (copy) {
       if (mine_at < free.y) {
         fresh = __ldcg(P.list + mine_at);
-        if (inside(P, mine_at, P.moves)) P.src[mine_at] = P.rows[(long long)i * width + full], P.dst[mine_at] = fresh;
+        const int from = P.rows[(long long)i * width + full];
+        if (!in_pool(P, from)) raise(P, kBadPage);  // (the copy leaves it out)
+        if (inside(P, mine_at, P.moves)) P.src[mine_at] = from, P.dst[mine_at] = fresh;
         if (inside(P, fresh, P.t.pages)) P.t.refs[fresh] = 1;
       } else {  // no page left for the copy: it ends up empty
         raise(P, kOutOfPages);

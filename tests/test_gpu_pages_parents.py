@@ -30,3 +30,16 @@ def test_the_cache_names_the_call_that_left_a_page_out():
     with pytest.raises(csa.CSAError, match="copy_pages .*outside"):
         c.status()
     c.status()
+
+
+@pytest.mark.parametrize("sequences", [2, 100])
+@pytest.mark.parametrize("page", [10 ** 9, -1, 400])
+def test_a_page_outside_the_pool_that_is_only_copied_is_told(sequences, page):
+    """The parent keeps its row, which nobody looks at; the heir's copy of the last page is of none."""
+    t = csa.PageTable.allocate(4 * sequences, sequences, 4, 2)
+    t.extend(dev([3] + [0] * (sequences - 1)))
+    t.table[0, 1] = page
+    assert listed(t.fork(dev([0, 0] + list(range(2, sequences))))) == [(page, 2)]
+    assert t.table[1].tolist() == [0, 2, -1, -1] and t.lens.tolist()[:2] == [3, 3]
+    with pytest.raises(csa.CSAError, match="outside"):
+        t.status()
